@@ -286,6 +286,50 @@ AWQ_API awq_status_t awq_search_alpha_noalloc(const uint16_t* x, const uint16_t*
                                               const float* alphas, int n_alpha, double* err, int* best,
                                               awq_stream_t stream);
 
+/* Linear layers in 8-bit integers (W8A8), beside the W4A16 path: the weights quantized once per
+ * output channel, the activations per token at each call, both symmetric with 127 steps, after the
+ * same equivalent transform (CSDN "02.02 AWQ": weights times s, activations divided by s).
+ *
+ * awq_quantize_tokens: x' = fp16(x / s), or x with s = NULL; per row m (fp32, IEEE division)
+ *   sx_m = max_k |x'_mk| / 127,  xq_mk = rint(x'_mk / sx_m)   (half to even; -127..127).
+ *   x fp16 [M, K] row-major;  s fp32 [K] or NULL;  xq int8 [M, K];  sx fp32 [M].
+ * awq_quantize_channels: the same for the rows of w' = fp16(W * s) (W with fold_scale = NULL):
+ *   W fp16 [N, K];  wq int8 [N, K];  sw fp32 [N].
+ *   A row of zeros has step 0 and codes 0. A row with a NaN or an infinity has that step (NaN if
+ *   there is one) and codes 0, so every output that uses it is NaN.
+ * awq_w8a8_linear: y[m][n] = fp16(float(sum_k xq[m][k] * wq[n][k]) * (sx[m] * sw[n])), the sum exact
+ *   in int32; y fp16 [M, N]. Any int8 codes are allowed (-128 too). Bitwise reproducible.
+ *   Like the decode kernel it starts reading wq before the preceding kernel of `stream` has
+ *   completed (the prefetch rule of awq_w4a16_gemv, for which awq_quantize_channels lets no later
+ *   kernel start early); xq, sx and sw are read after it.
+ * Require M >= 1, N >= 1 (both at most 2^31 - 128), 16 <= K <= AWQ_INT8_MAX_K, K % 16 == 0; x, s, W,
+ * xq, wq and y 16-byte aligned. */
+#define AWQ_INT8_MAX_K 131056   /* (-128)^2 K < 2^31 */
+AWQ_API awq_status_t awq_quantize_tokens(const uint16_t* x, const float* s, int M, int K, int8_t* xq, float* sx,
+                                         awq_stream_t stream);
+AWQ_API awq_status_t awq_quantize_channels(const uint16_t* W, const float* fold_scale, int N, int K, int8_t* wq,
+                                           float* sw, awq_stream_t stream);
+AWQ_API awq_status_t awq_w8a8_linear(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, uint16_t* y,
+                                     int M, int N, int K, awq_stream_t stream);
+
+/* The residual update after a block and the RMS norm before the next one, with the activation
+ * scaling of the next quantized linear layer (the 1/s of awq_scale_activations):
+ *   t  = y, or with post_weight  y / sqrt(mean_k(y^2) + eps) * post_weight
+ *   h  = residual + alpha * gate * t
+ *   x  = h / sqrt(mean_k(h^2) + eps) * weight / s
+ * in fp32, each of h and x rounded once to fp16 (x is computed from the unrounded h).
+ *   y, residual, h, x  fp16 [M, K] row-major; residual NULL: 0; h NULL: not stored.
+ *   gate  fp16 [ceil(M / rows_per_gate), K] or NULL (1): row m uses gate row m / rows_per_gate
+ *         (rows_per_gate = 1: a gate per token; >= M: one row for all; in between: one per sequence).
+ *   post_weight, weight  fp16 [K] (post_weight may be NULL);  s fp32 [K] or NULL (1).
+ * Requires M >= 1, 8 <= K <= AWQ_NORM_MAX_K, K % 8 == 0, alpha finite, eps finite and >= 0, and
+ * rows_per_gate >= 1 where there is a gate; every pointer 16-byte aligned. */
+#define AWQ_NORM_MAX_K 32768
+AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, const uint16_t* gate,
+                                       int rows_per_gate, const uint16_t* post_weight, const uint16_t* weight,
+                                       const float* s, float alpha, float eps, int M, int K, uint16_t* h, uint16_t* x,
+                                       awq_stream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the device status word of the
  * current device. Returns AWQ_ERR_TIMEOUT if a kernel since the last poll gave
  * up a bounded wait (its outputs are then undefined), AWQ_ERR_CUDA if the

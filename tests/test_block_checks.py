@@ -1,0 +1,112 @@
+"""Argument checks of the 8-bit linear layer and the residual norm, on the CPU (no device call is made)."""
+import ctypes
+
+import pytest
+import torch
+
+import weight_only_quantization_w4a16_b200 as P
+
+V = ctypes.c_void_p
+A, MIS = 0x10000, 0x10008    # never dereferenced: every call below fails its checks first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from weight_only_quantization_w4a16_b200 import build as B
+    B.build()
+    return P.load_library()
+
+
+def test_row_quantizers_refuse_before_any_device_call(lib):
+    for fn in (lib.awq_quantize_tokens, lib.awq_quantize_channels):
+        assert fn(None, None, 1, 16, V(A), V(A), None) == 1
+        assert fn(V(A), None, 1, 16, None, V(A), None) == 1
+        assert fn(V(A), None, 1, 16, V(A), None, None) == 1
+        for rows, K in ((0, 16), (-1, 16), (1, 0), (1, 8), (1, 24), (1, 131072), (1, -16)):
+            assert fn(V(A), None, rows, K, V(A), V(A), None) == 1
+        assert fn(V(MIS), None, 1, 16, V(A), V(A), None) == 3
+        assert fn(V(A), V(MIS), 1, 16, V(A), V(A), None) == 3
+        assert fn(V(A), None, 1, 16, V(MIS), V(A), None) == 3
+        assert fn(V(A), None, 1, 16, V(A), V(A + 2), None) == 3
+
+
+def test_w8a8_refuses_before_any_device_call(lib):
+    fn = lib.awq_w8a8_linear
+    for i in range(5):
+        args = [V(A)] * 5
+        args[i] = None
+        assert fn(*args, 1, 1, 16, None) == 1
+    for M, N, K in ((0, 1, 16), (1, 0, 16), (1, 1, 0), (1, 1, 24), (1, 1, 131072), (2147483647, 1, 16), (1, 2147483647, 16)):
+        assert fn(*[V(A)] * 5, M, N, K, None) == 1
+    for i in (0, 2, 4):
+        args = [V(A)] * 5
+        args[i] = V(MIS)
+        assert fn(*args, 1, 1, 16, None) == 3
+    assert fn(V(A), V(A + 2), V(A), V(A), V(A), 1, 1, 16, None) == 3
+
+
+def _norm(lib, y=A, r=A, g=A, per=1, pw=A, w=A, s=A, alpha=1.0, eps=1e-6, M=1, K=8, h=A, x=A):
+    p = lambda v: None if v is None else V(v)  # noqa: E731
+    return lib.awq_residual_norm(p(y), p(r), p(g), per, p(pw), p(w), p(s), alpha, eps, M, K, p(h), p(x), None)
+
+
+def test_residual_norm_refuses_before_any_device_call(lib):
+    nan, inf = float("nan"), float("inf")
+    for bad in (dict(y=None), dict(w=None), dict(x=None), dict(M=0), dict(K=0), dict(K=12), dict(K=32776), dict(per=0),
+                dict(alpha=nan), dict(alpha=inf), dict(eps=nan), dict(eps=-1e-9), dict(eps=inf)):
+        assert _norm(lib, **bad) == 1, bad
+    for name in ("y", "r", "g", "pw", "w", "s", "h", "x"):
+        assert _norm(lib, **{name: MIS}) == 3, name
+
+
+def half(*shape):
+    return torch.zeros(shape, dtype=torch.float16)
+
+
+def test_binding_checks_of_the_row_quantizers():
+    ok = dict(require_cuda=False)
+    P.validate_quantize_rows(half(3, 32), torch.ones(32), torch.zeros((3, 32), dtype=torch.int8), torch.ones(3), **ok)
+    with pytest.raises(ValueError, match="multiple of 16"):
+        P.validate_quantize_rows(half(3, 24), None, torch.zeros((3, 24), dtype=torch.int8), torch.ones(3), **ok)
+    with pytest.raises(ValueError, match="at least one row"):
+        P.validate_quantize_rows(half(0, 32), None, torch.zeros((0, 32), dtype=torch.int8), torch.ones(0), **ok)
+    with pytest.raises(ValueError, match="K=32"):
+        P.validate_quantize_rows(half(3, 32), torch.ones(31), torch.zeros((3, 32), dtype=torch.int8), torch.ones(3), **ok)
+    with pytest.raises(ValueError, match="shape"):
+        P.validate_quantize_rows(half(3, 32), None, torch.zeros((2, 32), dtype=torch.int8), torch.ones(3), **ok)
+    with pytest.raises(ValueError, match="3 elements"):
+        P.validate_quantize_rows(half(3, 32), None, torch.zeros((3, 32), dtype=torch.int8), torch.ones(4), **ok)
+    with pytest.raises(TypeError, match="int8"):
+        P.validate_quantize_rows(half(3, 32), None, torch.zeros((3, 32), dtype=torch.uint8), torch.ones(3), **ok)
+    with pytest.raises(ValueError, match="contiguous"):
+        P.validate_quantize_rows(half(32, 3).t(), None, torch.zeros((3, 32), dtype=torch.int8), torch.ones(3), **ok)
+    with pytest.raises(ValueError, match="CUDA"):
+        P.awq_quantize_tokens(half(3, 32))
+
+
+def test_binding_checks_of_the_product():
+    xq, wq = torch.zeros((3, 32), dtype=torch.int8), torch.zeros((5, 32), dtype=torch.int8)
+    P.validate_w8a8(xq, torch.ones(3), wq, torch.ones(5), half(3, 5), require_cuda=False)
+    for bad, match in (((xq, torch.ones(4), wq, torch.ones(5), half(3, 5)), "sx"),
+                       ((xq, torch.ones(3), wq, torch.ones(4), half(3, 5)), "sw"),
+                       ((xq, torch.ones(3), wq, torch.ones(5), half(5, 3)), "shape"),
+                       ((xq, torch.ones(3), torch.zeros((5, 16), dtype=torch.int8), torch.ones(5), half(3, 5)), "columns")):
+        with pytest.raises(ValueError, match=match):
+            P.validate_w8a8(*bad, require_cuda=False)
+
+
+def test_binding_checks_of_the_norm():
+    def check(y=half(6, 16), residual=half(6, 16), weight=half(16), post=half(16), gate=half(2, 16), alpha=1.0, eps=1e-6,
+              s=torch.ones(16), h=half(6, 16), x=half(6, 16)):
+        P.validate_residual_norm(y, residual, weight, post, gate, alpha, eps, s, h, x, require_cuda=False)
+
+    check()
+    check(residual=None, post=None, gate=None, s=None, h=None)
+    for bad, match in ((dict(gate=half(4, 16)), "divides"), (dict(gate=half(2, 8)), "divides"), (dict(weight=half(8)), "weight"),
+                       (dict(post=half(8)), "post_weight"), (dict(residual=half(5, 16)), "residual"), (dict(x=half(6, 8)), "x must"),
+                       (dict(s=torch.ones(8)), "K=16"), (dict(alpha=float("nan")), "finite"), (dict(eps=-1.0), "negative"),
+                       (dict(y=half(6, 12)), "multiple of 8"), (dict(y=half(0, 16)), "row")):
+        with pytest.raises(ValueError, match=match):
+            check(**bad)
+    with pytest.raises(TypeError):
+        check(weight=None)

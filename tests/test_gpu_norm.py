@@ -1,0 +1,135 @@
+"""The residual update with its norms on the GPU against the 64-bit oracle.
+
+Bound per value: the fp32 mean of K squares (per-thread chains of at most 32 terms, two halving
+trees and K's reciprocal) is off by less than 48 2^-24 relative, its inverse root by half of that
+plus 2^-23, and the products and the division by s add under 8 roundings of 2^-24; together below
+2^-18 of t and of x. h adds t's error, a rounding of 2^-24 of h, and x carries h's error through the
+norm (its own share of the mean included, at most sqrt(mean square) again). fp16 outputs add 2^-11,
+or 2^-25 below the normal range.
+"""
+import numpy as np
+import pytest
+
+from oracle import block_oracle as B
+from gpu_util import dev, host, lib, torch_mod
+
+pytestmark = pytest.mark.gpu
+E32, E16, SUB = 2.0 ** -18, 2.0 ** -11, 2.0 ** -25
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch_mod().cuda.is_available():
+        pytest.skip("no CUDA device")
+    lib()
+
+
+def inputs(M, K, post, gates, scaled, seed=0):
+    rng = np.random.default_rng([M, K, seed])
+    n = lambda *s: rng.standard_normal(s)  # noqa: E731
+    y = n(M, K)
+    y[:, rng.permutation(K)[: max(1, K // 100)]] *= 20
+    return dict(y=y.astype(np.float16), residual=(2 * n(M, K)).astype(np.float16), weight=(1 + 0.1 * n(K)).astype(np.float16),
+                post_weight=(1 + 0.1 * n(K)).astype(np.float16) if post else None,
+                gate=n(gates, K).astype(np.float16) if gates else None,
+                s=np.exp(rng.uniform(-1.5, 1.5, K)).astype(np.float32) if scaled else None)
+
+
+def to_dev(a):
+    return {k: dev(v) if isinstance(v, np.ndarray) else v for k, v in a.items()}
+
+
+def check(got, a, what="", **kw):
+    h, x, t = B.residual_norm(**a, **kw)
+    eh = E32 * np.abs(t) + 2.0 ** -24 * np.abs(h)
+    gain = np.abs(np.asarray(a["weight"], np.float64)) / (1.0 if a["s"] is None else a["s"])
+    root = np.sqrt((h * h).mean(1, keepdims=True) + kw.get("eps", 1e-6))
+    ex = E32 * np.abs(x) + gain / root * (eh + np.abs(h) / root * np.sqrt((eh * eh).mean(1, keepdims=True)))
+    for out, ref, e, name in ((got[0], h, eh, "h"), (got[1], x, ex, "x")):
+        if out is None:
+            continue
+        d = np.abs(host(out).astype(np.float64) - ref)
+        bad = ~(d <= e * (1 + E16) + E16 * np.abs(ref) + SUB)
+        assert not bad.any(), f"{what} {name}: {bad.sum()} of {bad.size} beyond the bound, first at {np.argwhere(bad)[0]}"
+
+
+@pytest.mark.parametrize("M,K", [(1, 8), (1, 4096), (3, 264), (5, 4104), (2, 8192), (4, 11016), (2, 16384), (3, 16392),
+                                 (1, 28672), (2, 32768), (300, 512)])
+@pytest.mark.parametrize("post,gate,scaled", [(False, "none", False), (True, "one", True), (False, "row", True), (True, "row", False)])
+def test_norm(M, K, post, gate, scaled):
+    P = lib()
+    a = inputs(M, K, post, {"none": 0, "one": 1, "row": M}[gate], scaled)
+    check(P.awq_residual_norm(**to_dev(a), alpha=0.7, eps=1e-5), a, f"M={M} K={K}", alpha=0.7, eps=1e-5)
+
+
+def test_gate_per_sequence_no_residual_and_no_h():
+    P = lib()
+    a = inputs(12, 1024, True, 3, True)
+    check(P.awq_residual_norm(**to_dev(a), alpha=-1.5), a, "3 sequences of 4 rows", alpha=-1.5)
+    a["residual"] = None
+    h, x = P.awq_residual_norm(**to_dev(a), want_h=False)
+    assert h is None
+    check((h, x), a, "no residual")
+
+
+def test_rows_of_zeros_and_large_values():
+    P = lib()
+    a = inputs(4, 512, True, 1, False)
+    a["y"][1] = 0
+    a["residual"][1] = 0                         # h = 0: x = 0
+    a["y"][2] = 60000 * np.sign(a["y"][2].astype(np.float32)).astype(np.float16)
+    a["residual"][3] = 30000                     # squares beyond the fp16 range
+    got = P.awq_residual_norm(**to_dev(a))
+    check(got, a, "zeros and large values")
+    assert (host(got[0])[1] == 0).all() and (host(got[1])[1] == 0).all()
+    a["y"][0, 3] = np.nan
+    h, x = (host(v) for v in P.awq_residual_norm(**to_dev(a)))
+    assert np.isnan(h[0]).all() and np.isnan(x[0]).all() and np.isfinite(x[1:]).all()
+    a["post_weight"] = None
+    h, x = (host(v) for v in P.awq_residual_norm(**to_dev(a)))
+    assert np.isnan(h[0]).sum() == 1 and np.isnan(x[0]).all()
+
+
+def test_zero_rows_without_eps_and_alpha_zero():
+    P = lib()
+    a = inputs(2, 64, False, 0, False)
+    check(P.awq_residual_norm(**to_dev(a), alpha=0.0, eps=0.0), a, "alpha 0", alpha=0.0, eps=0.0)
+
+
+def test_rows_do_not_depend_on_the_batch_and_repeat():
+    torch, P = torch_mod(), lib()
+    a = inputs(64, 4096, True, 64, True)
+    d = to_dev(a)
+    h, x = P.awq_residual_norm(**d)
+    h2, x2 = P.awq_residual_norm(**d)
+    assert torch.equal(h, h2) and torch.equal(x, x2)
+    one = {k: v[5:6].contiguous() if k in ("y", "residual", "gate") else v for k, v in d.items()}
+    h1, x1 = P.awq_residual_norm(**one)
+    assert torch.equal(h1[0], h[5]) and torch.equal(x1[0], x[5])
+
+
+def test_captured_chain_into_a_quantized_layer():
+    """norm -> int8 layer -> norm in a CUDA graph, replayed with new inputs, equals the eager calls."""
+    torch, P = torch_mod(), lib()
+    K, M = 1024, 9
+    rng = np.random.default_rng(3)
+    W = (rng.standard_normal((K, K)) * 0.02).astype(np.float16)
+    layer = P.AWQInt8Linear.from_float(dev(W), dev(rng.standard_normal((32, K)).astype(np.float16)))
+    w = torch.ones(K, dtype=torch.float16, device="cuda")
+    y, r = (torch.zeros((M, K), dtype=torch.float16, device="cuda") for _ in range(2))
+
+    def block():
+        h, x = P.awq_residual_norm(y, r, w)       # the layer divides by its own s
+        return (h, *P.awq_residual_norm(layer(x), h, w, post_weight=w, alpha=0.5))
+
+    block()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = block()
+    for seed in range(3):
+        y.copy_(dev(np.random.default_rng([seed, 0]).standard_normal((M, K)).astype(np.float16)))
+        r.copy_(dev(np.random.default_rng([seed, 1]).standard_normal((M, K)).astype(np.float16)))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, block()))

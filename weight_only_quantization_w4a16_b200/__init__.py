@@ -17,6 +17,9 @@ Functions (same names as the C ABI):
 * ``awq_w4a16_linear_qkv(x, qweight, scales, zeros, Nq, Nkv)`` -> (q, k, v): fused q/k/v split
 * ``awq_w4a16_linear_silu_mul(x, qweight, scales, zeros, I)`` -> h = SiLU(gate) * up
 * ``awq_search_alpha(x, W, alphas)`` -> (err[n] float64, best index): the AWQ scale search
+* ``awq_quantize_tokens(x, s)`` -> (xq int8, sx fp32); ``awq_quantize_channels(W, fold_scale)`` -> (wq, sw)
+* ``awq_w8a8_linear(xq, sx, wq, sw)`` -> y[M,N] fp16: the product in 8-bit integers; class ``AWQInt8Linear``
+* ``awq_residual_norm(y, residual, weight, ...)`` -> (h, x'): residual update, RMS norms, activation scaling
 * ``awq_poll_device_status()``, test hooks ``awq_debug_set_wait_budget_ns(ns)``,
   ``awq_debug_drop_first_copy(enable)``, ``awq_debug_set_gemm_split(ks)``
 """
@@ -73,6 +76,10 @@ _SIGS = {
     "awq_w4a16_linear_silu_mul": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP], _I),
     "awq_search_alpha": ([_VP, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I),
     "awq_search_alpha_noalloc": ([_VP, _VP, _I, _I, _I, _VP, _I, _VP, _VP, _VP], _I),
+    "awq_quantize_tokens": ([_VP, _VP, _I, _I, _VP, _VP, _VP], _I),
+    "awq_quantize_channels": ([_VP, _VP, _I, _I, _VP, _VP, _VP], _I),
+    "awq_w8a8_linear": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP], _I),
+    "awq_residual_norm": ([_VP, _VP, _VP, _I, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float, _I, _I, _VP, _VP, _VP], _I),
     "awq_debug_set_wait_budget_ns": ([ctypes.c_ulonglong], _I),
     "awq_debug_drop_first_copy": ([_I], _I),
     "awq_debug_set_gemm_split": ([_I], _I),
@@ -484,3 +491,173 @@ def awq_scale_activations(x, s, x_scaled=None):
     st = load_library().awq_scale_activations(_ptr(x), _ptr(s), M, K, _ptr(x_scaled), _stream_ptr())
     _check("awq_scale_activations", st)
     return x_scaled
+
+
+# ---------------------------------------------------------------------------- 8-bit integer linear layers
+INT8_MAX_K = 131056
+
+
+def _check_int8_k(K: int):
+    if K < 16 or K % 16 or K > INT8_MAX_K:
+        raise ValueError(f"K must be a multiple of 16 in [16, {INT8_MAX_K}], got {K}")
+
+
+def validate_quantize_rows(x, s, q, step, require_cuda=True, names=("x", "s", "xq", "sx")):
+    torch = _torch()
+    _need(x, torch.float16, names[0], 2, require_cuda=require_cuda)
+    rows, K = x.shape
+    if rows < 1:
+        raise ValueError(f"{names[0]} must have at least one row")
+    _check_int8_k(K)
+    if s is not None:
+        _check_vec(s, K, names[1], require_cuda)
+    _need(q, torch.int8, names[2], 2, require_cuda=require_cuda)
+    if tuple(q.shape) != (rows, K):
+        raise ValueError(f"{names[2]} must have shape {(rows, K)}, got {tuple(q.shape)}")
+    _need(step, torch.float32, names[3], 1, require_cuda=require_cuda)
+    if step.numel() != rows:
+        raise ValueError(f"{names[3]} must have {rows} elements, got {step.numel()}")
+
+
+def _quantize_rows(fn_name: str, x, s, out, names):
+    torch = _torch()
+    _need(x, torch.float16, names[0], 2)
+    rows, K = x.shape
+    if out is None:
+        out = (torch.empty((rows, K), dtype=torch.int8, device=x.device),
+               torch.empty(rows, dtype=torch.float32, device=x.device))
+    q, step = out
+    validate_quantize_rows(x, s, q, step, names=names)
+    st = getattr(load_library(), fn_name)(_ptr(x), _ptr(s), rows, K, _ptr(q), _ptr(step), _stream_ptr())
+    _check(fn_name, st)
+    return q, step
+
+
+def awq_quantize_tokens(x, s=None, out=None):
+    """x' = fp16(x / s) (x itself without s) in 8 bits per token: (xq int8 [M, K], sx fp32 [M])."""
+    return _quantize_rows("awq_quantize_tokens", x, s, out, ("x", "s", "xq", "sx"))
+
+
+def awq_quantize_channels(W, fold_scale=None, out=None):
+    """w' = fp16(W * fold_scale) in 8 bits per output channel: (wq int8 [N, K], sw fp32 [N])."""
+    return _quantize_rows("awq_quantize_channels", W, fold_scale, out, ("W", "fold_scale", "wq", "sw"))
+
+
+def validate_w8a8(xq, sx, wq, sw, y, require_cuda=True):
+    torch = _torch()
+    _need(xq, torch.int8, "xq", 2, require_cuda=require_cuda)
+    _need(wq, torch.int8, "wq", 2, require_cuda=require_cuda)
+    (M, K), N = xq.shape, wq.shape[0]
+    if M < 1 or N < 1:
+        raise ValueError("xq and wq must have at least one row")
+    if wq.shape[1] != K:
+        raise ValueError(f"wq must have K={K} columns, got {wq.shape[1]}")
+    _check_int8_k(K)
+    _check_vec(sx, M, "sx", require_cuda)
+    _check_vec(sw, N, "sw", require_cuda)
+    _need(y, torch.float16, "y", 2, require_cuda=require_cuda)
+    if tuple(y.shape) != (M, N):
+        raise ValueError(f"y must have shape {(M, N)}, got {tuple(y.shape)}")
+
+
+def awq_w8a8_linear(xq, sx, wq, sw, y=None):
+    """y[M, N] = fp16((xq . wq^T) * sx * sw), the integer sums exact (tcgen05 int8)."""
+    torch = _torch()
+    _need(xq, torch.int8, "xq", 2)
+    _need(wq, torch.int8, "wq", 2)
+    (M, K), N = xq.shape, wq.shape[0]
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.float16, device=xq.device)
+    validate_w8a8(xq, sx, wq, sw, y)
+    st = load_library().awq_w8a8_linear(_ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), _ptr(y), M, N, K, _stream_ptr())
+    _check("awq_w8a8_linear", st)
+    return y
+
+
+class AWQInt8Linear:
+    """A linear layer in 8-bit integers: codes and steps per output channel, and the stored scale s
+    (or None) that its activations are divided by.
+
+    ``AWQInt8Linear.from_float(W, x_calib)`` takes s from the activation statistic of ``x_calib``
+    and quantizes the folded weight; ``layer(x)`` quantizes the tokens and multiplies.
+    """
+
+    def __init__(self, wq, sw, s=None):
+        torch = _torch()
+        _need(wq, torch.int8, "wq", 2)
+        self.N, self.K = wq.shape
+        if self.N < 1:
+            raise ValueError("wq must have at least one row")
+        _check_int8_k(self.K)
+        _check_vec(sw, self.N, "sw")
+        if s is not None:
+            _check_vec(s, self.K, "s")
+        self.wq, self.sw, self.s = wq, sw, s
+
+    @classmethod
+    def from_float(cls, W, x_calib=None, alpha: float = 0.5):
+        s = None if x_calib is None else awq_activation_scale(x_calib, alpha, want_scaled=False)[0]
+        wq, sw = awq_quantize_channels(W, s)
+        return cls(wq, sw, s)
+
+    def __call__(self, x, y=None):
+        xq, sx = awq_quantize_tokens(x, self.s)
+        return awq_w8a8_linear(xq, sx, self.wq, self.sw, y)
+
+
+# ---------------------------------------------------------------------------- residual update and norms
+NORM_MAX_K = 32768
+
+
+def validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x, require_cuda=True):
+    torch = _torch()
+    _need(y, torch.float16, "y", 2, require_cuda=require_cuda)
+    M, K = y.shape
+    if M < 1:
+        raise ValueError("y must have at least one row")
+    if K < 8 or K % 8 or K > NORM_MAX_K:
+        raise ValueError(f"K must be a multiple of 8 in [8, {NORM_MAX_K}], got {K}")
+    for t, name in ((residual, "residual"), (h, "h"), (x, "x")):
+        if t is not None:
+            _need(t, torch.float16, name, 2, require_cuda=require_cuda)
+            if tuple(t.shape) != (M, K):
+                raise ValueError(f"{name} must have shape {(M, K)}, got {tuple(t.shape)}")
+    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
+        if t is not None or name == "weight":
+            _need(t, torch.float16, name, 1, require_cuda=require_cuda)
+            if t.numel() != K:
+                raise ValueError(f"{name} must have K={K} elements, got {t.numel()}")
+    if gate is not None:
+        _need(gate, torch.float16, "gate", 2, require_cuda=require_cuda)
+        if gate.shape[1] != K or gate.shape[0] < 1 or M % gate.shape[0]:
+            raise ValueError(f"gate must have K={K} columns and a number of rows that divides M={M}, "
+                             f"got {tuple(gate.shape)}")
+    if s is not None:
+        _check_vec(s, K, "s", require_cuda)
+    if not (-3.0e38 <= alpha <= 3.0e38) or not (0.0 <= eps <= 3.0e38):
+        raise ValueError("alpha must be finite, and eps finite and not negative")
+
+
+def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, s=None,
+                      out=None, want_h: bool = True):
+    """Residual update after a block and RMS norm before the next one; returns (h, x').
+
+    h = residual + alpha * gate * t with t = y, or y normalised and times ``post_weight`` if given;
+    x' = rmsnorm(h) * weight / s. ``residual`` may be None (0); ``gate`` is None (1) or [G, K] with G a
+    divisor of M: row m uses gate row m // (M // G). ``s`` is the next layer's stored scale.
+    ``want_h=False`` leaves h unstored (the first result is None)."""
+    torch = _torch()
+    _need(y, torch.float16, "y", 2)
+    M, K = y.shape
+    if out is None:
+        out = (torch.empty_like(y) if want_h else None, torch.empty_like(y))
+    h, x = out
+    alpha, eps = float(alpha), float(eps)
+    if x is None:
+        raise ValueError("x is always written")
+    validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
+    per = M // gate.shape[0] if gate is not None else 1
+    st = load_library().awq_residual_norm(_ptr(y), _ptr(residual), _ptr(gate), per, _ptr(post_weight), _ptr(weight),
+                                          _ptr(s), alpha, eps, M, K, _ptr(h), _ptr(x), _stream_ptr())
+    _check("awq_residual_norm", st)
+    return h, x

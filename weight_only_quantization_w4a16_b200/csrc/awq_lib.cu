@@ -16,6 +16,8 @@
 #include "awq_common.cuh"
 #include "awq_gemm.cuh"
 #include "awq_gemv.cuh"
+#include "awq_int8.cuh"
+#include "awq_norm.cuh"
 #include "awq_quant.cuh"
 #include "awq_search.cuh"
 #include "awq_w4a16.h"
@@ -534,6 +536,123 @@ awq_status_t launch_gemm(const __half* x, const uint32_t* qw, const __half* sc, 
   return launch_gemm_epi<kEpiPlain>(x, qw, sc, zr, epi, M, N, K, dev, num_sms, stream);
 }
 
+// --------------------------------------------------------------------------- int8 dispatch
+// One row per CTA: as many values per thread in registers as keep the CTA at 1024 threads at most.
+template <int MODE, bool kWeights>
+awq_status_t launch_quantize_rows(const __half* x, const float* s, int rows, int K, int8_t* q, float* step,
+                                  cudaStream_t stream) {
+  const int chunks = K / 8;
+  const dim3 grid(static_cast<unsigned>(rows), 1, 1), none(0, 0, 0);
+  auto run = [&](auto kernel, int vpt) {
+    const int threads = std::min(1024, round_up(ceil_div(chunks, vpt), 32));
+    return launch_ex(kernel, grid, dim3(threads, 1, 1), none, 0, stream, x, s, K, q, step);
+  };
+  if (chunks <= 512) return run(awq_quantize_rows_kernel<MODE, 1, kWeights>, 1);
+  if (chunks <= 2048) return run(awq_quantize_rows_kernel<MODE, 2, kWeights>, 2);
+  if (chunks <= 4096) return run(awq_quantize_rows_kernel<MODE, 4, kWeights>, 4);
+  return run(awq_quantize_rows_kernel<MODE, 0, kWeights>, 4);
+}
+
+// Codes [rows, K] int8 row-major as a 2-D tensor, box {128 k, box_rows}, 128-byte swizzle, zero fill.
+awq_status_t make_i8_map(CUtensorMap* map, const void* q, int rows, int K, int box_rows) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return AWQ_ERR_CUDA;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? AWQ_OK : AWQ_ERR_CUDA;
+}
+
+// Token tile, weight rows per tile and K split of the int8 kernel. A CTA's time is modelled in
+// cycles per 128-byte k block: the larger of its share of the HBM stream (rows * 128 bytes at 23
+// bytes per cycle and SM) and of its four MMAs per 128 rows (at least 47 cycles each to issue, BT / 2
+// at full rate), plus a fixed cost per tile and per cluster exchange. With M <= 64 the rows per tile
+// are chosen so that all SMs share the weight rows evenly; above, tiles are 128 rows.
+struct Int8Plan {
+  int bt, mt, rows, ks;
+};
+Int8Plan int8_plan(int M, int N, int K, int num_sms) {
+  const int KB = ceil_div(K, 128);
+  Int8Plan best = {256, 1, 128, 1};
+  double best_cost = 1e300;
+  auto consider = [&](int bt, int rows, int ks) {
+    const int mt = rows > 128 ? 2 : 1;
+    const long long tiles = static_cast<long long>(ceil_div(N, rows)) * ceil_div(M, bt);
+    const long long slots = std::max(1, num_sms / ks);
+    const double mma = 4.0 * mt * std::max(47.0, bt / 2.0);
+    const double stream = rows * 128.0 / 23.0;
+    const double cost = static_cast<double>((tiles + slots - 1) / slots) *
+                        (ceil_div(KB, ks) * std::max(mma, stream) + 600.0 + 2.0 * bt + (ks > 1 ? 1500.0 : 0.0));
+    if (cost < best_cost) { best_cost = cost; best = {bt, mt, rows, ks}; }
+  };
+  for (int ks = 1; ks <= 8 && ks <= KB && ks <= num_sms; ks *= 2) {
+    if (M <= 64) {
+      const long long slots = num_sms / ks;
+      const long long rounds = (N + slots * 256 - 1) / (slots * 256);
+      const int rows = std::min(256, round_up(static_cast<int>((N + slots * rounds - 1) / (slots * rounds)), 8));
+      if (ks > 1 && rounds > 1) continue;
+      consider(M <= 16 ? 16 : M <= 32 ? 32 : 64, rows, ks);
+    } else {
+      consider(64, 128, ks);
+      consider(128, 128, ks);
+      if (M > 128) consider(256, 128, ks);
+    }
+  }
+  return best;
+}
+
+template <int BT, int MT>
+awq_status_t launch_w8a8_cfg(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, __half* y, int M,
+                             int N, int K, const Int8Plan& p, int dev, int num_sms, cudaStream_t stream) {
+  auto kernel = awq_w8a8_kernel<BT, MT>;
+  static std::atomic<uint64_t> smem_done{0};
+  awq_status_t st = ensure_smem(kernel, kI8SmemMax, dev, smem_done);
+  if (st != AWQ_OK) return st;
+  Int8Args a = {sx, sw, y, M, N, K, p.rows, ceil_div(N, p.rows), ceil_div(M, BT), p.ks, 0, 0};
+  const int KB = ceil_div(K, 128), steps = ceil_div(KB, p.ks);
+  const int block = (p.rows + BT) * 128;
+  a.kpb = std::max(1, std::min(std::min(4, steps), 24576 / block));
+  const int pad = MT * 16384 - p.rows * 128;
+  a.stages = std::min(kI8MaxStages, (kI8SmemMax - kI8Fixed - pad) / (a.kpb * block));
+  const long long tiles = static_cast<long long>(a.row_blocks) * a.tok_tiles;
+  if (tiles * p.ks > (1ll << 30)) return AWQ_ERR_INVALID_ARG;
+  const size_t smem = static_cast<size_t>(a.stages) * a.kpb * block + pad + kI8Fixed;
+  CUtensorMap wmap, xmap;
+  if ((st = make_i8_map(&wmap, wq, N, K, p.rows)) != AWQ_OK) return st;
+  if ((st = make_i8_map(&xmap, xq, M, K, BT)) != AWQ_OK) return st;
+  const long long grid = p.ks > 1 ? tiles * p.ks : std::min<long long>(tiles, num_sms);
+  return launch_ex(kernel, dim3(static_cast<unsigned>(grid), 1, 1), dim3(kI8Threads, 1, 1),
+                   p.ks > 1 ? dim3(p.ks, 1, 1) : dim3(0, 0, 0), smem, stream, wmap, xmap, a);
+}
+
+awq_status_t launch_w8a8(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, __half* y, int M, int N,
+                         int K, int dev, int num_sms, cudaStream_t stream) {
+  const Int8Plan p = int8_plan(M, N, K, num_sms);
+#define AWQ_I8_ARGS xq, sx, wq, sw, y, M, N, K, p, dev, num_sms, stream
+  switch (p.bt * 4 + p.mt) {
+    case 16 * 4 + 1: return launch_w8a8_cfg<16, 1>(AWQ_I8_ARGS);
+    case 16 * 4 + 2: return launch_w8a8_cfg<16, 2>(AWQ_I8_ARGS);
+    case 32 * 4 + 1: return launch_w8a8_cfg<32, 1>(AWQ_I8_ARGS);
+    case 32 * 4 + 2: return launch_w8a8_cfg<32, 2>(AWQ_I8_ARGS);
+    case 64 * 4 + 1: return launch_w8a8_cfg<64, 1>(AWQ_I8_ARGS);
+    case 64 * 4 + 2: return launch_w8a8_cfg<64, 2>(AWQ_I8_ARGS);
+    case 128 * 4 + 1: return launch_w8a8_cfg<128, 1>(AWQ_I8_ARGS);
+    default: return launch_w8a8_cfg<256, 1>(AWQ_I8_ARGS);
+  }
+#undef AWQ_I8_ARGS
+}
+
+// Row-quantizer arguments (tokens and channels alike).
+awq_status_t check_rows_args(const void* x, const void* s, int rows, int K, const void* q, const void* step) {
+  if (!x || !q || !step || rows < 1 || K < 16 || K % 16 != 0 || K > AWQ_INT8_MAX_K) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(s) || !aligned16(q) || (reinterpret_cast<uintptr_t>(step) & 3u)) return AWQ_ERR_MISALIGNED;
+  return AWQ_OK;
+}
+
 // Rows are limited so that every count below fits an int: N <= 2^31 - 2^7 and N * K <= 2^34.
 constexpr long long kMaxRows = (1ll << 31) - 128;
 inline bool rows_ok(int N, int K) {
@@ -877,6 +996,80 @@ awq_status_t awq_w4a16_linear_silu_mul(const uint16_t* x, const uint32_t* qweigh
     if (st != AWQ_ERR_UNSUPPORTED) return st;
   }
   return launch_gemm_epi<kEpiSiluMul>(xh, qweight, sh, zeros, epi, M, 2 * I, K, dev, sms, cs);
+}
+
+awq_status_t awq_quantize_tokens(const uint16_t* x, const float* s, int M, int K, int8_t* xq, float* sx,
+                                 awq_stream_t stream) {
+  awq_status_t st = check_rows_args(x, s, M, K, xq, sx);
+  if (st != AWQ_OK) return st;
+  int dev, sms;
+  if ((st = current_device(&dev, &sms)) != AWQ_OK) return st;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const __half* xh = reinterpret_cast<const __half*>(x);
+  return s != nullptr ? launch_quantize_rows<kRowDivide, false>(xh, s, M, K, xq, sx, cs)
+                      : launch_quantize_rows<kRowPlain, false>(xh, s, M, K, xq, sx, cs);
+}
+
+awq_status_t awq_quantize_channels(const uint16_t* W, const float* fold_scale, int N, int K, int8_t* wq, float* sw,
+                                   awq_stream_t stream) {
+  awq_status_t st = check_rows_args(W, fold_scale, N, K, wq, sw);
+  if (st != AWQ_OK) return st;
+  int dev, sms;
+  if ((st = current_device(&dev, &sms)) != AWQ_OK) return st;
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const __half* wh = reinterpret_cast<const __half*>(W);
+  return fold_scale != nullptr ? launch_quantize_rows<kRowMultiply, true>(wh, fold_scale, N, K, wq, sw, cs)
+                               : launch_quantize_rows<kRowPlain, true>(wh, fold_scale, N, K, wq, sw, cs);
+}
+
+awq_status_t awq_w8a8_linear(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, uint16_t* y, int M,
+                             int N, int K, awq_stream_t stream) {
+  if (!xq || !sx || !wq || !sw || !y) return AWQ_ERR_INVALID_ARG;
+  if (M < 1 || N < 1 || N > kMaxRows || K < 16 || K % 16 != 0 || K > AWQ_INT8_MAX_K) return AWQ_ERR_INVALID_ARG;
+  if (M > kMaxRows) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(sx) & 3u) ||
+      (reinterpret_cast<uintptr_t>(sw) & 3u))
+    return AWQ_ERR_MISALIGNED;
+  int dev, sms;
+  const awq_status_t st = current_device(&dev, &sms);
+  if (st != AWQ_OK) return st;
+  return launch_w8a8(xq, sx, wq, sw, reinterpret_cast<__half*>(y), M, N, K, dev, sms,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, const uint16_t* gate, int rows_per_gate,
+                               const uint16_t* post_weight, const uint16_t* weight, const float* s, float alpha,
+                               float eps, int M, int K, uint16_t* h, uint16_t* x, awq_stream_t stream) {
+  if (!y || !weight || !x || M < 1 || K < 8 || K % 8 != 0 || K > AWQ_NORM_MAX_K) return AWQ_ERR_INVALID_ARG;
+  if (gate != nullptr && rows_per_gate < 1) return AWQ_ERR_INVALID_ARG;
+  if (!(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f || !(eps >= 0.0f) || eps > 3.0e38f) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(y) || !aligned16(residual) || !aligned16(gate) || !aligned16(post_weight) || !aligned16(weight) ||
+      !aligned16(s) || !aligned16(h) || !aligned16(x))
+    return AWQ_ERR_MISALIGNED;
+  int dev, sms;
+  const awq_status_t st = current_device(&dev, &sms);
+  if (st != AWQ_OK) return st;
+  NormArgs a;
+  a.y = reinterpret_cast<const __half*>(y);
+  a.residual = reinterpret_cast<const __half*>(residual);
+  a.gate = reinterpret_cast<const __half*>(gate);
+  a.post_w = reinterpret_cast<const __half*>(post_weight);
+  a.w = reinterpret_cast<const __half*>(weight);
+  a.s = s;
+  a.h = reinterpret_cast<__half*>(h);
+  a.x = reinterpret_cast<__half*>(x);
+  a.K = K;
+  a.rows_per_gate = rows_per_gate;
+  a.alpha = alpha;
+  a.eps = eps;
+  const int chunks = K / 8;
+  auto run = [&](auto kernel, int vpt) {
+    return launch_ex(kernel, dim3(static_cast<unsigned>(M), 1, 1), dim3(round_up(ceil_div(chunks, vpt), 32), 1, 1),
+                     dim3(0, 0, 0), 0, reinterpret_cast<cudaStream_t>(stream), a);
+  };
+  if (chunks <= 512) return run(awq_residual_norm_kernel<1>, 1);
+  if (chunks <= 2048) return run(awq_residual_norm_kernel<2>, 2);
+  return run(awq_residual_norm_kernel<4>, 4);
 }
 
 awq_status_t awq_poll_device_status(awq_stream_t stream) {
