@@ -330,6 +330,30 @@ AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residu
                                        const float* s, float alpha, float eps, int M, int K, uint16_t* h, uint16_t* x,
                                        awq_stream_t stream);
 
+/* A whole mixture-of-experts layer for a few tokens (decode), experts in packed 4-bit weights:
+ *   l_te = sum_k x_tk router_ek (fp32); the top_k experts of token t by l, ties to the lowest index;
+ *   p_te = softmax over all E experts of l_t at the chosen ones, divided by their sum if renormalize;
+ *   h    = p_te * SiLU(x_t . Wgate_e^T) * (x_t . Wup_e^T) / h_scale_e      (fp32, rounded to fp16)
+ *   y_t  = sum over the chosen e of h . Wdown_e^T                          (fp32 sums, fp16 output)
+ *   x       fp16 [T, K], already divided by the gate/up layers' s (awq_scale_activations,
+ *           awq_residual_norm); router fp16 [E, K], multiplied by the same s.
+ *   gate_up E packed layers of 2*I x K (I gate rows, then I up rows) in packed layout v2, one after
+ *           another: each array is E times awq_*_bytes(2*I, K) long. down: E packed layers of K x I.
+ *   h_scale fp32 [E, I] or NULL (1): the down layers' s.   y fp16 [T, K].
+ *   workspace: device, 16-byte aligned, awq_moe_workspace_bytes bytes; its contents before the call
+ *           do not matter. Calls that may overlap on the GPU need workspaces of their own.
+ * Only the chosen experts' weights are read. A logit that is NaN ranks below every number.
+ * Two kernels; the second is a cooperative launch with one CTA on every SM and a bounded wait on the
+ * others between the two layers (AWQ_ERR_TIMEOUT). Bitwise reproducible.
+ * Requires 1 <= T <= 32, 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I multiples of 128, each
+ * expert's layers within awq_*_bytes' limits; every pointer 16-byte aligned. */
+AWQ_API size_t awq_moe_workspace_bytes(int T, int E, int K, int I, int top_k);
+AWQ_API awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint32_t* gate_up_qweight,
+                                   const uint16_t* gate_up_scales, const uint8_t* gate_up_zeros,
+                                   const uint32_t* down_qweight, const uint16_t* down_scales, const uint8_t* down_zeros,
+                                   const float* h_scale, int T, int E, int K, int I, int top_k, int renormalize,
+                                   uint16_t* y, void* workspace, size_t workspace_bytes, awq_stream_t stream);
+
 /* Synchronizes `stream`, then reads and clears the device status word of the
  * current device. Returns AWQ_ERR_TIMEOUT if a kernel since the last poll gave
  * up a bounded wait (its outputs are then undefined), AWQ_ERR_CUDA if the

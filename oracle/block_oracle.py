@@ -48,3 +48,51 @@ def residual_norm(y, residual, weight, post_weight=None, gate=None, alpha=1.0, e
     h = t + (0.0 if residual is None else np.asarray(residual, f64))
     x = h / np.sqrt((h * h).mean(1, keepdims=True) + eps) * np.asarray(weight, f64)
     return h, x if s is None else x / np.asarray(s, f64), t
+
+
+def silu(v):
+    with np.errstate(over="ignore"):
+        return v / (1.0 + np.exp(-v))
+
+
+def route(x, router, top, renormalize):
+    """(ids [T, top], p [T, top]) by the logits in 64 bits, ties to the lowest index; and the smallest
+    distance between a chosen logit and one that is not (infinite if all are chosen)."""
+    logits = np.asarray(x, f64) @ np.asarray(router, f64).T
+    order = np.argsort(-logits, axis=1, kind="stable")
+    ids = order[:, :top]
+    e = np.exp(logits - logits.max(1, keepdims=True))
+    p = np.take_along_axis(e, ids, 1)
+    p = p / (p if renormalize else e).sum(1, keepdims=True)
+    gap = np.inf
+    if top < logits.shape[1]:
+        l = np.take_along_axis(logits, order, 1)
+        gap = (l[:, top - 1] - l[:, top]).min()
+    return ids, p, gap
+
+
+def moe(x, router, gate_up, down, top, renormalize, h_scale=None):
+    """(y, bound) of the layer with dequantized experts gate_up [E, 2I, K], down [E, K, I].
+
+    bound: the error that the definition's roundings allow. h is rounded to fp16 (half a step, 2^-11,
+    or 2^-25 below the normal range); sums of products in fp32 on tensor cores are taken as off by at
+    most 2^-18 of the sum of magnitudes, p, SiLU and the division by h_scale as off by 2^-18; y is
+    rounded to fp16 at the end."""
+    x = np.asarray(x, f64)
+    I = down.shape[2]
+    ids, p, gap = route(x, router, top, renormalize)
+    y, err = np.zeros_like(x), np.zeros_like(x)
+    for t in range(x.shape[0]):
+        for e, w in zip(ids[t], p[t]):
+            gu, mag = gate_up[e] @ x[t], np.abs(gate_up[e]) @ np.abs(x[t])
+            g, u = gu[:I], gu[I:]
+            s = 1.0 if h_scale is None else np.asarray(h_scale[e], f64)
+            h = w * silu(g) * u / s
+            sig = 1.0 / (1.0 + np.exp(-np.clip(g, -700, 700)))
+            slope = np.abs(sig * (1.0 + g * (1.0 - sig)))
+            dh = w / s * 2.0 ** -18 * (slope * np.abs(u) * mag[:I] + np.abs(silu(g)) * mag[I:])
+            dh = dh + np.abs(h) * (2.0 ** -16 + 2.0 ** -11) + 2.0 ** -25
+            a = np.abs(down[e])
+            y[t] += down[e] @ h
+            err[t] += a @ dh + 2.0 ** -18 * (a @ np.abs(h))
+    return y, err + 2.0 ** -11 * (np.abs(y) + err) + 2.0 ** -25, gap

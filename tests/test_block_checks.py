@@ -110,3 +110,56 @@ def test_binding_checks_of_the_norm():
             check(**bad)
     with pytest.raises(TypeError):
         check(weight=None)
+
+
+# ---------------------------------------------------------------------------- mixture of experts
+def _moe(lib, ptr=None, value=None, T=1, E=8, K=256, I=128, top=2, ws=None):
+    """One call with pointer argument `ptr` (by position) replaced; the first nine may be checked."""
+    p = [V(A)] * 8 + [None]
+    if ptr is not None and ptr < 9:
+        p[ptr] = value
+    y, w = (value if ptr == 9 else V(A)), (value if ptr == 10 else V(A))
+    need = lib.awq_moe_workspace_bytes(T, E, K, I, top)
+    return lib.awq_moe_w4a16(*p, T, E, K, I, top, 1, y, w, need if ws is None else ws, None)
+
+
+def test_moe_refuses_before_any_device_call(lib):
+    need = lib.awq_moe_workspace_bytes(1, 8, 256, 128, 2)
+    assert need > 0
+    for i in list(range(8)) + [9, 10]:
+        assert _moe(lib, i, None) == 1, i
+        assert _moe(lib, i, V(MIS)) == 3, i
+    assert _moe(lib, 8, V(MIS)) == 3
+    assert _moe(lib, ws=need - 1) == 1
+    for bad in (dict(T=0), dict(T=33), dict(E=0), dict(E=513), dict(E=1), dict(top=0), dict(top=17), dict(top=9), dict(K=0),
+                dict(K=192), dict(I=0), dict(I=64), dict(I=-128), dict(I=1 << 30, K=1 << 20)):
+        sizes = {**dict(T=1, E=8, K=256, I=128, top=2), **bad}
+        assert lib.awq_moe_workspace_bytes(sizes["T"], sizes["E"], sizes["K"], sizes["I"], sizes["top"]) == 0, bad
+        assert _moe(lib, ws=1 << 40, **bad) == 1, bad
+
+
+def _stack(E, N, K, dtype=torch.int32):
+    qb, sb, zb = P._packed_sizes_host(N, K)
+    return (torch.zeros((E, qb // 4), dtype=dtype), torch.zeros((E, sb // 2), dtype=torch.float16),
+            torch.zeros((E, zb), dtype=torch.uint8))
+
+
+def test_binding_checks_of_the_experts():
+    def check(router=half(8, 256), gate_up=_stack(8, 256, 256), down=_stack(8, 256, 128), I=128, top=2, hs=None):
+        return P._validate_moe_weights(router, gate_up, down, I, top, hs, require_cuda=False)
+
+    assert check() == (8, 256) and check(hs=torch.ones(8, 128)) == (8, 256)
+    for bad, match in ((dict(top=0), "top_k"), (dict(top=9), "top_k"), (dict(router=half(4, 256)), "shape"),
+                       (dict(gate_up=_stack(8, 128, 256)), "gate_up"), (dict(down=_stack(7, 256, 128)), "down"),
+                       (dict(gate_up=_stack(8, 256, 256)[:2]), "gate_up"), (dict(I=64), "multiples of 128"),
+                       (dict(router=half(8, 200)), "multiples of 128"), (dict(hs=torch.ones(8, 127)), "h_scale"),
+                       (dict(router=half(513, 256)), "experts")):
+        with pytest.raises(ValueError, match=match):
+            check(**bad)
+    with pytest.raises(TypeError, match="int32"):
+        check(gate_up=_stack(8, 256, 256, torch.int64))
+    P._validate_moe_tokens(half(32, 256), half(32, 256), 8, 256, require_cuda=False)
+    for x, y, match in ((half(33, 256), None, "tokens"), (half(0, 256), None, "tokens"), (half(3, 128), None, "K=256"),
+                        (half(3, 256), half(2, 256), "shape")):
+        with pytest.raises(ValueError, match=match):
+            P._validate_moe_tokens(x, y, 8, 256, require_cuda=False)

@@ -20,6 +20,8 @@ Functions (same names as the C ABI):
 * ``awq_quantize_tokens(x, s)`` -> (xq int8, sx fp32); ``awq_quantize_channels(W, fold_scale)`` -> (wq, sw)
 * ``awq_w8a8_linear(xq, sx, wq, sw)`` -> y[M,N] fp16: the product in 8-bit integers; class ``AWQInt8Linear``
 * ``awq_residual_norm(y, residual, weight, ...)`` -> (h, x'): residual update, RMS norms, activation scaling
+* ``awq_moe_w4a16(x, router, gate_up, down, I, top_k)`` -> y[T,K]: a mixture-of-experts layer for a few
+  tokens, experts in packed weights; class ``AWQMoE``
 * ``awq_poll_device_status()``, test hooks ``awq_debug_set_wait_budget_ns(ns)``,
   ``awq_debug_drop_first_copy(enable)``, ``awq_debug_set_gemm_split(ks)``
 """
@@ -80,6 +82,8 @@ _SIGS = {
     "awq_quantize_channels": ([_VP, _VP, _I, _I, _VP, _VP, _VP], _I),
     "awq_w8a8_linear": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP], _I),
     "awq_residual_norm": ([_VP, _VP, _VP, _I, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float, _I, _I, _VP, _VP, _VP], _I),
+    "awq_moe_workspace_bytes": ([_I, _I, _I, _I, _I], ctypes.c_size_t),
+    "awq_moe_w4a16": ([_VP] * 9 + [_I] * 6 + [_VP, _VP, ctypes.c_size_t, _VP], _I),
     "awq_debug_set_wait_budget_ns": ([ctypes.c_ulonglong], _I),
     "awq_debug_drop_first_copy": ([_I], _I),
     "awq_debug_set_gemm_split": ([_I], _I),
@@ -661,3 +665,128 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
                                           _ptr(s), alpha, eps, M, K, _ptr(h), _ptr(x), _stream_ptr())
     _check("awq_residual_norm", st)
     return h, x
+
+
+# ---------------------------------------------------------------------------- mixture of experts
+MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 32, 512, 16
+
+
+def _validate_moe_weights(router, gate_up, down, I: int, top_k: int, h_scale, require_cuda=True):
+    """Checks the layer's weights; returns (E, K)."""
+    torch = _torch()
+    _need(router, torch.float16, "router", 2, require_cuda=require_cuda)
+    E, K = router.shape
+    if not 1 <= E <= MOE_MAX_EXPERTS:
+        raise ValueError(f"the number of experts must be in [1, {MOE_MAX_EXPERTS}], got {E}")
+    if not 1 <= top_k <= min(E, MOE_MAX_TOP_K):
+        raise ValueError(f"top_k must be in [1, {min(E, MOE_MAX_TOP_K)}], got {top_k}")
+    if K < GROUP_SIZE or K % GROUP_SIZE or I < GROUP_SIZE or I % GROUP_SIZE:
+        raise ValueError("K and I must be positive multiples of 128")
+    for packed, what, (N, Kin) in ((gate_up, "gate_up", (2 * I, K)), (down, "down", (K, I))):
+        if len(packed) != 3:
+            raise ValueError(f"{what} must be (qweight, scales, zeros)")
+        qb, sb, zb = _packed_sizes_host(N, Kin)
+        for t, dtype, size, name in zip(packed, (torch.int32, torch.float16, torch.uint8), (qb // 4, sb // 2, zb),
+                                        ("qweight", "scales", "zeros")):
+            _need(t, dtype, f"{what} {name}", 2, require_cuda=require_cuda)
+            if tuple(t.shape) != (E, size):
+                raise ValueError(f"{what} {name} must have shape {(E, size)}, got {tuple(t.shape)}")
+    if h_scale is not None:
+        _need(h_scale, torch.float32, "h_scale", 2, require_cuda=require_cuda)
+        if tuple(h_scale.shape) != (E, I):
+            raise ValueError(f"h_scale must have shape {(E, I)}, got {tuple(h_scale.shape)}")
+    return E, K
+
+
+def _validate_moe_tokens(x, y, E: int, K: int, require_cuda=True):
+    torch = _torch()
+    _need(x, torch.float16, "x", 2, require_cuda=require_cuda)
+    T = x.shape[0]
+    if not 1 <= T <= MOE_MAX_TOKENS:
+        raise ValueError(f"the number of tokens must be in [1, {MOE_MAX_TOKENS}], got {T}")
+    if x.shape[1] != K:
+        raise ValueError(f"x must have K={K} columns, got {x.shape[1]}")
+    if y is not None:
+        _need(y, torch.float16, "y", 2, require_cuda=require_cuda)
+        if tuple(y.shape) != (T, K):
+            raise ValueError(f"y must have shape {(T, K)}, got {tuple(y.shape)}")
+
+
+def _moe_call(x, router, gate_up, down, E, K, I, top_k, renormalize, h_scale, y, workspace):
+    torch = _torch()
+    lib = load_library()
+    T = x.shape[0]
+    need = int(lib.awq_moe_workspace_bytes(T, E, K, I, top_k))
+    if need == 0:
+        raise ValueError("shape out of range for the mixture-of-experts layer")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        _need(workspace, torch.uint8, "workspace", 1)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must hold {need} bytes")
+    if y is None:
+        y = torch.empty_like(x)
+    st = lib.awq_moe_w4a16(_ptr(x), _ptr(router), *[_ptr(t) for t in gate_up], *[_ptr(t) for t in down], _ptr(h_scale),
+                           T, E, K, I, top_k, int(bool(renormalize)), _ptr(y), _ptr(workspace), workspace.numel(),
+                           _stream_ptr())
+    _check("awq_moe_w4a16", st)
+    return y
+
+
+def awq_moe_w4a16(x, router, gate_up, down, I: int, top_k: int, renormalize: bool = True, h_scale=None, y=None,
+                  workspace=None):
+    """A whole mixture-of-experts layer for up to 32 tokens: router, top-k, experts, weighted sum.
+
+    x [T, K] fp16; router [E, K] fp16; gate_up and down: (qweight, scales, zeros) with the experts'
+    packed arrays stacked along a first dimension (gate_up: 2 I x K layers, I gate rows then I up
+    rows; down: K x I); h_scale [E, I] fp32 divides the intermediate (the down layers' s)."""
+    I, top_k = int(I), int(top_k)
+    E, K = _validate_moe_weights(router, gate_up, down, I, top_k, h_scale)
+    _validate_moe_tokens(x, y, E, K)
+    return _moe_call(x, router, gate_up, down, E, K, I, top_k, renormalize, h_scale, y, workspace)
+
+
+class AWQMoE:
+    """A mixture-of-experts layer with packed 4-bit experts (decode, up to 32 tokens a call).
+
+    ``AWQMoE.from_float(router, W_gate_up, W_down, top_k, x_calib)`` takes one scale s for the router
+    and the gate/up layers from the activation statistic of ``x_calib`` (they share their input),
+    folds and quantizes every expert; ``layer(x)`` scales the activations by 1/s (skipped with
+    ``scaled=True``, for an x that awq_residual_norm has already divided) and runs the layer.
+    """
+
+    def __init__(self, router, gate_up, down, I: int, top_k: int, renormalize: bool = True, h_scale=None, s=None):
+        self.I, self.top_k, self.renormalize = int(I), int(top_k), bool(renormalize)
+        self.E, self.K = _validate_moe_weights(router, gate_up, down, self.I, self.top_k, h_scale)
+        if s is not None:
+            _check_vec(s, self.K, "s")
+        self.router, self.gate_up, self.down, self.h_scale, self.s = router, tuple(gate_up), tuple(down), h_scale, s
+
+    @classmethod
+    def from_float(cls, router, W_gate_up, W_down, top_k: int, x_calib=None, alpha: float = 0.5, renormalize: bool = True,
+                   h_scale=None):
+        """W_gate_up [E, 2 I, K], W_down [E, K, I], router [E, K], all fp16; h_scale [E, I] or None is
+        folded into the down layers and divides their input."""
+        torch = _torch()
+        _need(W_gate_up, torch.float16, "W_gate_up", 3)
+        _need(W_down, torch.float16, "W_down", 3)
+        E, I2, K = W_gate_up.shape
+        if tuple(W_down.shape) != (E, K, I2 // 2) or I2 % 2:
+            raise ValueError(f"W_gate_up [E, 2 I, K] and W_down [E, K, I] disagree: {tuple(W_gate_up.shape)}, "
+                             f"{tuple(W_down.shape)}")
+        s = None
+        if x_calib is not None:
+            s, _ = awq_activation_scale(x_calib, alpha, want_scaled=False)
+            router = (router.float() * s).half()
+        stack = lambda layers: tuple(torch.stack(t) for t in zip(*layers))  # noqa: E731
+        gate_up = stack([awq_quantize_g128(W_gate_up[e], s) for e in range(E)])
+        down = stack([awq_quantize_g128(W_down[e], None if h_scale is None else h_scale[e]) for e in range(E)])
+        return cls(router, gate_up, down, I2 // 2, top_k, renormalize, h_scale, s)
+
+    def __call__(self, x, y=None, workspace=None, scaled: bool = False):
+        _validate_moe_tokens(x, y, self.E, self.K)
+        if self.s is not None and not scaled:
+            x = awq_scale_activations(x, self.s)
+        return _moe_call(x, self.router, self.gate_up, self.down, self.E, self.K, self.I, self.top_k, self.renormalize,
+                         self.h_scale, y, workspace)
