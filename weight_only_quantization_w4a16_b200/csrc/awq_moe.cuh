@@ -18,9 +18,9 @@
 // through one ring without waiting for the barrier, so phase 2's first weights arrive while phase 1
 // ends. The consumer warps split a unit's group pairs and use the exact integer dequantization and
 // warp MMAs of the decode kernel; activations are read through L1, the columns of an MMA being the
-// expert's own tokens in phase 1 and all tokens in phase 2 (zero where a token did not choose the
-// expert), so phase 2 sums over experts in its accumulators. h carries p: its fp16 rounding
-// (2^-12 of each term on average) is the one the unfused layers make between their calls.
+// expert's own tokens. Phase 2 adds an expert's columns to its tokens' places in the warp's record.
+// h carries p: its fp16 rounding (2^-12 of each term on average) is the one the unfused layers make
+// between their calls.
 // Partial sums of the warps are added in warp order: results repeat bit for bit.
 #pragma once
 
@@ -172,39 +172,148 @@ struct MoeArgs {
   int T, E, K, I, top;
 };
 
-constexpr int kMoeCW = 8;                       // consumer warps
-constexpr int kMoeThreads = 32 * (kMoeCW + 1);
-constexpr int kMoeStageItems = 16;              // (tile, group pair) items per ring stage
+constexpr int kMoeCW = 16;                      // consumer warps
+constexpr int kMoeThreads = 32 * (kMoeCW + 2);  // + producer, + epilogue
+constexpr int kMoeStageItems = 16;              // (tile, group pair) items per ring stage, one per consumer warp
 constexpr int kMoeOffS = kMoeStageItems * kPairCodeBytes;
 constexpr int kMoeOffZ = kMoeOffS + kMoeStageItems * kPairScaleBytes;
 constexpr int kMoeStage = kMoeOffZ + kMoeStageItems * kPairZeroBytes;   // 34048 bytes
 static_assert(kMoeStage % 128 == 0, "ring stages stay aligned");
 
-// MT: 8-token tiles (T <= 8 MT). A record is one warp's fp32 sums of one 16-row tile, [column][20]
+// MTT: 8-token tiles (T <= 8 MTT). A record is one warp's fp32 sums of one 16-row tile, [column][20]
 // (20: rows padded so that the fragment stores hit distinct banks).
-template <int MT>
+template <int MTT>
 struct MoeCfg {
-  static constexpr int kStages = 3;
-  static constexpr int kRec = 8 * MT * 20;              // floats
-  static constexpr int kBufs = MT == 1 ? 4 : 2;         // units whose records are held at a time
-  static constexpr int kDone = kBufs / 2;               // units that may end within one stage
+  static constexpr int kStages = MTT == 4 ? 3 : 4;
+  static constexpr int kBlock = MTT == 1 ? 2 : 1;       // tiles per warp that share activation fragments
+  static constexpr int kRec = 8 * MTT * 20;             // floats
+  static constexpr int kBufs = MTT == 4 ? 1 : 2;        // record buffers (two tiles each)
   static constexpr int kRecBytes = kBufs * kMoeCW * 2 * kRec * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kBufs + 1;
 };
 
+// How a strip (one tile of one expert, Q group pairs along its K) is cut into stages. Up to 8 pairs:
+// `strips` strips share a stage, `wide` warps each. More: `chunks` stages of up to `len` pairs.
+struct MoeCut {
+  int Q, wide, strips, chunks, len;
+  __device__ explicit MoeCut(int q) : Q(q) {
+    wide = q <= 1 ? 1 : q <= 2 ? 2 : q <= 4 ? 4 : q <= 8 ? 8 : 16;
+    strips = kMoeStageItems / wide;
+    chunks = (q + kMoeStageItems - 1) / kMoeStageItems;
+    len = (q + chunks - 1) / chunks;
+  }
+};
+
+// Sums of the activation fragments over a group, by an MMA whose A operand is all ones: lane (r, t)
+// gets those of its accumulator columns 2t and 2t+1.
+template <int MT>
+__device__ __forceinline__ void moe_sums(float (&xs)[MT][2], const uint4 (&xv)[2][MT][2]) {
+  const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    float d[4];
+    mma_m16n8k16_f32_zero(d, ones, xv[0][j][0].x, xv[0][j][0].y);
+    mma_m16n8k16_f32(d, ones, xv[0][j][0].z, xv[0][j][0].w);
+    mma_m16n8k16_f32(d, ones, xv[0][j][1].x, xv[0][j][1].y);
+    mma_m16n8k16_f32(d, ones, xv[0][j][1].z, xv[0][j][1].w);
+    mma_m16n8k16_f32(d, ones, xv[1][j][0].x, xv[1][j][0].y);
+    mma_m16n8k16_f32(d, ones, xv[1][j][0].z, xv[1][j][0].w);
+    mma_m16n8k16_f32(d, ones, xv[1][j][1].x, xv[1][j][1].y);
+    mma_m16n8k16_f32(d, ones, xv[1][j][1].z, xv[1][j][1].w);
+    xs[j][0] = d[0];
+    xs[j][1] = d[1];
+  }
+}
+
+// acc += S (sum x q - z sum x) for one group. A code pair masked out of its word is a pair of fp16
+// subnormals q 2^-24 (16 q 2^-24 in the odd nibbles, rows r+8): one AND makes an operand of the MMA,
+// whose products are exact. The zero point costs no instruction per code: it enters once per group
+// with the group's activation sum. 66 instructions per 2048 weights, where subtracting it from
+// every code pair takes about 130 and made the integer pipe the bound.
+template <int MT>
+__device__ __forceinline__ void moe_group(float (&acc)[MT][4], const uint4& c0, const uint4& c1,
+                                          const uint4 (&xv)[2][MT][2], const float (&xs)[MT][2], uint32_t sv, uint32_t zz) {
+  float tq[MT][4];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const uint4& wv = kk ? c1 : c0;
+#pragma unroll
+    for (int s4 = 0; s4 < 4; ++s4) {
+      const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
+      const uint32_t q8 = __umulhi(q, 1u << 24);   // q >> 8 on the multiply pipe
+      const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const uint4& xq = xv[kk][j][s4 >> 1];
+        const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
+        if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[j], a, b0, b1);
+        else mma_m16n8k16_f32(tq[j], a, b0, b1);
+      }
+    }
+  }
+  const float2 sf = half2_bits_to_float2(sv);
+  const float s_lo = sf.x * 16777216.0f, s_hi = sf.y * 1048576.0f;   // 2^24 and 2^20: exact
+  const float z_lo = -sf.x * small_uint_to_float(zz & 0xFu), z_hi = -sf.y * small_uint_to_float(zz >> 4);
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    acc[j][0] += fmaf(s_lo, tq[j][0], z_lo * xs[j][0]);
+    acc[j][1] += fmaf(s_lo, tq[j][1], z_lo * xs[j][1]);
+    acc[j][2] += fmaf(s_hi, tq[j][2], z_hi * xs[j][0]);
+    acc[j][3] += fmaf(s_hi, tq[j][3], z_hi * xs[j][1]);
+  }
+}
+
+// The activation fragments of one group pair for one 8-token tile, and their sums per group.
+struct MoeFrag {
+  uint4 v[2][2][2];   // [group][64-k tile][half]
+  float s[2][2];      // [group][column 2t, 2t+1]
+};
+
+// One group pair with at most 8 tokens: the two groups' MMA chains run side by side.
+__device__ __forceinline__ void moe_pair(float (&acc)[4], const uint4 (&w)[2][2], const MoeFrag& f, const uint32_t (&sv)[2],
+                                         const uint32_t (&zz)[2]) {
+  float tq[2][4];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int s4 = 0; s4 < 4; ++s4)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint4& wv = w[g][kk];
+        const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
+        const uint32_t q8 = __umulhi(q, 1u << 24);   // q >> 8 on the multiply pipe
+        const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
+        const uint4& xq = f.v[g][kk][s4 >> 1];
+        const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
+        if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[g], a, b0, b1);
+        else mma_m16n8k16_f32(tq[g], a, b0, b1);
+      }
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float2 sf = half2_bits_to_float2(sv[g]);
+    const float s_lo = sf.x * 16777216.0f, s_hi = sf.y * 1048576.0f;   // 2^24 and 2^20: exact
+    const float z_lo = -sf.x * small_uint_to_float(zz[g] & 0xFu), z_hi = -sf.y * small_uint_to_float(zz[g] >> 4);
+    acc[0] += fmaf(s_lo, tq[g][0], z_lo * f.s[g][0]);
+    acc[1] += fmaf(s_lo, tq[g][1], z_lo * f.s[g][1]);
+    acc[2] += fmaf(s_hi, tq[g][2], z_hi * f.s[g][0]);
+    acc[3] += fmaf(s_hi, tq[g][3], z_hi * f.s[g][1]);
+  }
+}
+
 // Bytes of the routing lists: expert counts, active experts, first slots (+1), assignment experts,
-// slot tokens, slot weights, and the 16-bit slot map.
+// slot tokens, slot weights.
 __host__ __device__ inline int moe_list_bytes(int T, int E, int top) {
   const int n = T * top, act = n < E ? n : E;
-  return (E + 2 * act + 1 + 3 * n) * 4 + act * T * 2;
+  return (E + 2 * act + 1 + 3 * n) * 4;
 }
 template <int MT>
 __host__ __device__ inline int moe_smem_bytes(int T, int E, int top) {
   using C = MoeCfg<MT>;
-  return C::kStages * kMoeStage + C::kRecBytes + (2 * C::kStages + 1) * 8 + 8 + moe_list_bytes(T, E, top);
+  return C::kStages * kMoeStage + C::kRecBytes + C::kBars * 8 + 8 + moe_list_bytes(T, E, top);
 }
 __device__ __forceinline__ uint4 ld_coherent_v4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
@@ -216,8 +325,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
   float* rec = reinterpret_cast<float*>(smem + S * kMoeStage);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kMoeStage + C::kRecBytes);
   uint64_t* empty = full + S;
-  uint64_t* cbar = empty + S;                  // the consumer warps' barrier
-  volatile int* s_abort = reinterpret_cast<volatile int*>(cbar + 1);
+  uint64_t* rfull = empty + S;                 // record buffers
+  uint64_t* rempty = rfull + C::kBufs;
+  uint64_t* go = rempty + C::kBufs;            // phase 2 may read h
+  volatile int* s_abort = reinterpret_cast<volatile int*>(go + 1);
   int* s_active = const_cast<int*>(s_abort) + 1;
   const int n_assign = a.T * a.top;
   const int max_act = min(n_assign, a.E);
@@ -227,7 +338,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
   int* l_ids = l_first + max_act + 1;          // [n_assign]
   int* l_token = l_ids + n_assign;             // [n_assign]: token of a slot
   float* l_p = reinterpret_cast<float*>(l_token + n_assign);   // [n_assign]: weight of a slot
-  int16_t* l_map = reinterpret_cast<int16_t*>(l_p + n_assign); // [max_act][T]: slot of (active index, token) or -1
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -235,7 +345,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kMoeCW);
     }
-    mbar_init(cbar, kMoeCW);
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&rfull[b], kMoeCW);
+      mbar_init(&rempty[b], 1);
+    }
+    mbar_init(go, 1);
     *s_abort = 0;
     mbar_fence_init();
   }
@@ -243,9 +357,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
   pdl_wait();
   const unsigned long long budget = g_wait_budget_ns;
 
-  // ---- the experts that are chosen, their slots (token order) and the slot of each (expert, token)
+  // ---- the experts that are chosen and their slots (token order)
   for (int i = threadIdx.x; i < a.E; i += kMoeThreads) l_count[i] = 0;
-  for (int i = threadIdx.x; i < max_act * a.T; i += kMoeThreads) l_map[i] = -1;
   __syncthreads();
   for (int i = threadIdx.x; i < n_assign; i += kMoeThreads) {
     const int e = a.ids[i];
@@ -287,285 +400,414 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
     const int slot = l_first[idx] + rank;
     l_token[slot] = i / a.top;
     l_p[slot] = a.p[i];
-    l_map[idx * a.T + i / a.top] = static_cast<int16_t>(slot);
   }
   __syncthreads();
 
-  // ---- this CTA's work. Phase 1: units are (active expert, 16-row gate tile + up tile), items its
-  // group pairs. Phase 2: units are 16-row output tiles, items (active expert, group pair).
+  // ---- this CTA's work. Phase 1: units (active expert, 16-row gate tile and its up tile). Phase 2:
+  // 16-row output tiles, over all active experts. All roles walk the same stages in the same order.
   const int A = *s_active, P = a.I / 16;
   const int G1 = a.K / kGroup, G2 = a.I / kGroup;
-  const int Q1 = (G1 + 1) / 2, Q2 = (G2 + 1) / 2;        // group pairs along K and along I
+  const MoeCut k1((G1 + 1) / 2), k2((G2 + 1) / 2);
   const int c0 = blockIdx.x, nc = gridDim.x;
   auto share = [&](int units, int c) { return static_cast<int>(static_cast<long long>(units) * c / nc); };
   const int u1a = share(A * P, c0), u1b = share(A * P, c0 + 1);
   const int u2a = share(a.K / 16, c0), u2b = share(a.K / 16, c0 + 1);
-  const int ipu1 = Q1, ipu2 = A * Q2;                     // items per unit
-  // a stage holds items of one phase, so many that at most kDone units end within it
-  const int len1 = min(kMoeStageItems / 2, C::kDone * ipu1), len2 = min(kMoeStageItems, C::kDone * ipu2);
-  const int n1 = (u1b - u1a) * ipu1, n2 = (u2b - u2a) * ipu2;
+  constexpr int BL = C::kBlock;
+  int slot = 0;
+  uint32_t phase = 0;
+  auto advance = [&]() {
+    if (++slot == S) { slot = 0; phase ^= 1; }
+  };
+  int ev = 0;                                  // record events so far
+  auto buf_of = [&]() { return ev % C::kBufs; };
+  auto buf_parity = [&]() { return static_cast<uint32_t>((ev / C::kBufs) & 1); };
+  auto rec_of = [&](int w, int half) { return rec + ((buf_of() * kMoeCW + w) * 2 + half) * C::kRec; };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, s_abort, budget));
+  };
 
   if (warp == kMoeCW) {
     // ---------------------------------------------------------------- producer lane
-    if (lane == 0) {
-      int slot = 0, issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      // `n` items from (tile, pair) index tp of the packed layers into places at..at+n-1 of the stage
-      auto copy = [&](uint8_t* sb, int at, const uint8_t* q, const uint8_t* s, const uint8_t* z, size_t tp, int n,
-                      size_t total, uint64_t* bar) {
-        if (!AWQ_CHECK(n >= 1 && at >= 0 && at + n <= kMoeStageItems && tp + n <= total)) return;
-        bulk_g2s(sb + at * kPairCodeBytes, q + tp * kPairCodeBytes, n * kPairCodeBytes, bar);
-        bulk_g2s(sb + kMoeOffS + at * kPairScaleBytes, s + tp * kPairScaleBytes, n * kPairScaleBytes, bar);
-        bulk_g2s(sb + kMoeOffZ + at * kPairZeroBytes, z + tp * kPairZeroBytes, n * kPairZeroBytes, bar);
-      };
-      constexpr int kItem = kPairCodeBytes + kPairScaleBytes + kPairZeroBytes;
-      auto next = [&]() -> uint8_t* {
-        if (!mbar_wait_bounded(&empty[slot], phase ^ 1, s_abort, budget)) return nullptr;
-        return smem + slot * kMoeStage;
-      };
-      auto advance = [&]() {
-        ++issued;
-        if (++slot == S) { slot = 0; phase ^= 1; }
-      };
-      for (int i = 0; ok && i < n1; i += len1) {
-        const int n = min(len1, n1 - i);
-        uint8_t* sb = next();
-        if (sb == nullptr) { ok = false; break; }
-        mbar_arrive_expect_tx(&full[slot], 2 * n * kItem);
-        for (int d = 0; d < n;) {                          // runs within one expert are contiguous
-          const int u = u1a + (i + d) / ipu1, pr = (i + d) % ipu1;
-          const int x = u / P, j = u - x * P;
-          const int run = min(n - d, (P - j) * ipu1 - pr);
-          const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
-          copy(sb, d, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>(j) * Q1 + pr, run, a.E * a.gu_pairs, &full[slot]);
-          copy(sb, kMoeStageItems / 2 + d, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>(P + j) * Q1 + pr, run,
-               a.E * a.gu_pairs, &full[slot]);
-          d += run;
+    if (lane != 0) return;
+    int issued = 0;
+    constexpr int kItem = kPairCodeBytes + kPairScaleBytes + kPairZeroBytes;
+    uint8_t* sb = nullptr;
+    auto open = [&](int items) -> bool {
+      if (!mbar_wait_bounded(&empty[slot], phase ^ 1, s_abort, budget)) return false;
+      sb = smem + slot * kMoeStage;
+      mbar_arrive_expect_tx(&full[slot], items * kItem);
+      return true;
+    };
+    // `n` items from (tile, pair) index tp of the packed layers into places at..at+n-1 of the stage
+    auto copy = [&](int at, const uint8_t* q, const uint8_t* s, const uint8_t* z, size_t tp, int n, size_t total) {
+      if (!AWQ_CHECK(n >= 1 && at >= 0 && at + n <= kMoeStageItems && tp + n <= total)) return;
+      bulk_g2s(sb + at * kPairCodeBytes, q + tp * kPairCodeBytes, n * kPairCodeBytes, &full[slot]);
+      bulk_g2s(sb + kMoeOffS + at * kPairScaleBytes, s + tp * kPairScaleBytes, n * kPairScaleBytes, &full[slot]);
+      bulk_g2s(sb + kMoeOffZ + at * kPairZeroBytes, z + tp * kPairZeroBytes, n * kPairZeroBytes, &full[slot]);
+    };
+    auto close = [&]() {
+      ++issued;
+      advance();
+    };
+    const size_t gu_total = a.E * a.gu_pairs, dn_total = a.E * a.dn_pairs;
+    auto produce = [&]() {
+      for (int u = u1a; u < u1b;) {
+        const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
+        const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
+        if (k1.strips == 1) {
+          for (int j0 = ja; j0 < jb; j0 += BL)
+            for (int c = 0; c < k1.chunks; ++c) {
+              const int p0 = c * k1.len, n = min(k1.len, k1.Q - p0);
+              for (int b = 0; b < 2 * min(BL, jb - j0); ++b) {
+                if (!open(n)) return;
+                copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j0 + (b >> 1)) * k1.Q + p0, n, gu_total);
+                close();
+              }
+            }
+        } else {
+          const int half = k1.strips / 2;
+          for (int j0 = ja; j0 < jb; j0 += half) {
+            const int n = min(half, jb - j0) * k1.Q;
+            if (!open(2 * n)) return;
+            for (int h = 0; h < 2; ++h)
+              copy(h * half * k1.Q, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>(h * P + j0) * k1.Q, n, gu_total);
+            close();
+          }
         }
-        advance();
+        u += jb - ja;
       }
-      for (int i = 0; ok && i < n2; i += len2) {
-        const int n = min(len2, n2 - i);
-        uint8_t* sb = next();
-        if (sb == nullptr) { ok = false; break; }
-        mbar_arrive_expect_tx(&full[slot], n * kItem);
-        for (int d = 0; d < n;) {
-          const int u = u2a + (i + d) / ipu2, r = (i + d) % ipu2;
-          const int x = r / Q2, pr = r - x * Q2;
-          const int run = min(n - d, Q2 - pr);
-          copy(sb, d, a.dn_q, a.dn_s, a.dn_z,
-               static_cast<size_t>(l_expert[x]) * a.dn_pairs + static_cast<size_t>(u) * Q2 + pr, run,
-               a.E * a.dn_pairs, &full[slot]);
-          d += run;
+      for (int t0 = u2a; t0 < u2b; t0 += BL)
+        for (int x0 = 0; x0 < A; x0 += k2.strips) {
+          const int m = min(k2.strips, A - x0);
+          for (int c = 0; c < k2.chunks; ++c) {
+            const int p0 = c * k2.len, n = min(k2.len, k2.Q - p0);
+            for (int b = 0; b < min(BL, u2b - t0); ++b) {
+              if (!open(m * n)) return;
+              for (int i = 0; i < m; ++i)
+                copy(i * n, a.dn_q, a.dn_s, a.dn_z,
+                     static_cast<size_t>(l_expert[x0 + i]) * a.dn_pairs + static_cast<size_t>(t0 + b) * k2.Q + p0, n, dn_total);
+              close();
+            }
+          }
         }
-        advance();
+    };
+    produce();
+    // drain: every copy this thread issued has landed before the CTA may exit
+    int never = 0;
+    for (int i = max(0, issued - S); i < issued; ++i)
+      mbar_wait_bounded(&full[i % S], static_cast<uint32_t>((i / S) & 1), &never, kDrainBudgetNs);
+    return;
+  }
+
+  if (warp == kMoeCW + 1) {
+    // ---------------------------------------------------------------- epilogue warp
+    auto sum = [&](int half, int w0, int nw, int col, int row) {
+      float v = 0.0f;
+#pragma unroll 4
+      for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
+      return v;
+    };
+    auto done = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rempty[buf_of()]);
+      ++ev;
+    };
+    bool ok = true;
+    for (int u = u1a; ok && u < u1b;) {
+      const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
+      const int first = l_first[x], cnt = l_first[x + 1] - first;
+      const int per = k1.strips == 1 ? 1 : k1.strips / 2;               // units per event
+      for (int j0 = ja; j0 < jb; j0 += per) {
+        ok = warp_wait(&rfull[buf_of()], buf_parity());
+        if (!ok) break;
+        const int nu = min(per, jb - j0);
+        for (int q = lane; q < 16 * nu * cnt; q += 32) {
+          const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
+          const int i_row = 16 * (j0 + i) + row;
+          if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
+          const bool one = k1.strips == 1;
+          const float g = one ? sum(0, 0, k1.len, col, row) : sum(0, i * k1.wide, k1.Q, col, row);
+          const float v = one ? sum(1, 0, k1.len, col, row) : sum(0, (per + i) * k1.wide, k1.Q, col, row);
+          float hv = silu_mul(g, v) * l_p[first + col];
+          if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
+          a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
+        }
+        done();
       }
-      // drain: every copy this thread issued has landed before the CTA may exit
-      int never = 0;
-      for (int i = max(0, issued - S); i < issued; ++i)
-        mbar_wait_bounded(&full[i % S], static_cast<uint32_t>((i / S) & 1), &never, kDrainBudgetNs);
+      u += jb - ja;
+    }
+    // grid-wide barrier: every CTA's h is written (release) and visible (acquire)
+    __threadfence();
+    __syncwarp();
+    if (ok && lane == 0) {
+      unsigned v;
+      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(a.barrier) : "memory");
+      const uint64_t t0 = globaltimer_ns();
+      while (true) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.barrier) : "memory");
+        if (v >= gridDim.x || *s_abort) break;
+        if (globaltimer_ns() - t0 > budget) {
+          *s_abort = 1;
+          atomicOr(&g_dev_status, kDevStatusTimeout);
+          break;
+        }
+      }
+      if (*s_abort == 0) mbar_arrive(go);
+    }
+    for (int t0 = u2a; ok && t0 < u2b; t0 += BL) {
+      ok = warp_wait(&rfull[buf_of()], buf_parity());
+      if (!ok) break;
+      const int rows = 16 * min(BL, u2b - t0);
+      for (int q = lane; q < rows * a.T; q += 32) {
+        const int row = q % rows, col = q / rows;
+        if (!AWQ_CHECK(16 * t0 + row < a.K)) continue;
+        a.y[static_cast<size_t>(col) * a.K + 16 * t0 + row] = __float2half_rn(sum(row >> 4, 0, kMoeCW, col, row & 15));
+      }
+      done();
     }
     return;
   }
 
   // ------------------------------------------------------------------ consumer warps
   const int r = lane >> 2, t = lane & 3;
-  int slot = 0;
-  uint32_t phase = 0;
-  float acc[2][MTT][4];
-  auto clear = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < MTT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[h][j][c] = 0.0f;
-  };
-  clear();
-  auto rec_of = [&](int unit, int w, int half) { return rec + (((unit % C::kBufs) * kMoeCW + w) * 2 + half) * C::kRec; };
-  // this warp's sums of `unit` become its record
-  auto flush = [&](int unit, int halves) {
-    for (int h = 0; h < halves; ++h) {
-      float* p = rec_of(unit, warp, h);
-#pragma unroll
-      for (int j = 0; j < MTT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) p[(8 * j + 2 * t + (c & 1)) * 20 + r + 8 * (c >> 1)] = h ? acc[1][j][c] : acc[0][j][c];
-    }
-    clear();
-  };
-  auto sum_of = [&](int unit, int half, int col, int row) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kMoeCW; ++w) v += rec_of(unit, w, half)[col * 20 + row];
-    return v;
-  };
-  auto wait_full = [&]() -> bool {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], phase, s_abort, budget));
+  const uint8_t* sb = nullptr;
+  auto take = [&]() -> bool {
+    sb = smem + slot * kMoeStage;
+    return warp_wait(&full[slot], phase);
   };
   auto release = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[slot]);
-    if (++slot == S) { slot = 0; phase ^= 1; }
+    advance();
+  };
+  auto rec_ready = [&]() { return warp_wait(&rempty[buf_of()], buf_parity() ^ 1); };
+  auto rec_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&rfull[buf_of()]);
+    ++ev;
+  };
+  // Fragments of an 8-token tile: `row` points at the lane's token (k 0), the group starts at k0.
+  auto load8 = [&](uint4 (&v)[2][2], const __half* row, int k0) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      v[kk][0] = ld_coherent_v4(row + k0 + kk * 64 + 16 * t);
+      v[kk][1] = ld_coherent_v4(row + k0 + kk * 64 + 16 * t + 8);
+    }
+  };
+  auto load_frag = [&](MoeFrag& f, const __half* row, int pr, int G) {
+    load8(f.v[0], row, pr * 256);
+    if (2 * pr + 1 < G) {
+      load8(f.v[1], row, pr * 256 + 128);
+    } else {                                   // the padding group: its codes and scales are zero
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.v[1][i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto sum_frag = [&](MoeFrag& f) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float d[4];
+      const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+      mma_m16n8k16_f32_zero(d, ones, f.v[g][0][0].x, f.v[g][0][0].y);
+      mma_m16n8k16_f32(d, ones, f.v[g][0][0].z, f.v[g][0][0].w);
+      mma_m16n8k16_f32(d, ones, f.v[g][0][1].x, f.v[g][0][1].y);
+      mma_m16n8k16_f32(d, ones, f.v[g][0][1].z, f.v[g][0][1].w);
+      mma_m16n8k16_f32(d, ones, f.v[g][1][0].x, f.v[g][1][0].y);
+      mma_m16n8k16_f32(d, ones, f.v[g][1][0].z, f.v[g][1][0].w);
+      mma_m16n8k16_f32(d, ones, f.v[g][1][1].x, f.v[g][1][1].y);
+      mma_m16n8k16_f32(d, ones, f.v[g][1][1].z, f.v[g][1][1].w);
+      f.s[g][0] = d[0];
+      f.s[g][1] = d[1];
+    }
+  };
+  auto scale_of = [&](int item, int g) {
+    return *reinterpret_cast<const uint32_t*>(sb + kMoeOffS + item * kPairScaleBytes + g * 32 + r * 4);
+  };
+  auto zero_of = [&](int item, int g) { return static_cast<uint32_t>(sb[kMoeOffZ + item * kPairZeroBytes + g * 8 + r]); };
+  auto code_of = [&](int item, int g, int kk) {
+    return *reinterpret_cast<const uint4*>(sb + item * kPairCodeBytes + g * 1024 + kk * 512 + lane * 16);
+  };
+  auto pair8 = [&](float (&acc)[4], const MoeFrag& f, int item) {
+    const uint4 w[2][2] = {{code_of(item, 0, 0), code_of(item, 0, 1)}, {code_of(item, 1, 0), code_of(item, 1, 1)}};
+    const uint32_t sv[2] = {scale_of(item, 0), scale_of(item, 1)}, zz[2] = {zero_of(item, 0), zero_of(item, 1)};
+    moe_pair(acc, w, f, sv, zz);
+  };
+  // More than 8 tokens: 16 at a time, group by group; the fragments do not stay in registers.
+  // `row_of(col)` is the lane's activation row for a column.
+  auto pair_many = [&](float (&acc)[MTT][4], int item, int pr, int G, int cnt, auto row_of) {
+    if constexpr (MTT > 1) {
+#pragma unroll
+      for (int b = 0; b < MTT / 2; ++b) {
+        if (16 * b >= cnt) break;
+        const __half* row[2] = {row_of(min(16 * b + r, cnt - 1)), row_of(min(16 * b + 8 + r, cnt - 1))};
+#pragma unroll 1
+        for (int g = 0; g < 2 && 2 * pr + g < G; ++g) {
+          uint4 v[2][2][2];                    // [64-k tile][token tile][half]
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint4 one[2][2];
+            load8(one, row[m], pr * 256 + g * 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i >> 1][m][i & 1] = one[i >> 1][i & 1];
+          }
+          float xs[2][2];
+          moe_sums<2>(xs, v);
+          moe_group<2>(reinterpret_cast<float(&)[2][4]>(acc[2 * b]), code_of(item, g, 0), code_of(item, g, 1), v, xs,
+                       scale_of(item, g), zero_of(item, g));
+        }
+      }
+    }
   };
   bool ok = true;
-  // The consumer warps' barrier, bounded like every wait: false once any warp has given up.
-  uint32_t cphase = 0;
-  auto consumer_sync = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(cbar);
-    const bool done = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(cbar, cphase, s_abort, budget));
-    cphase ^= 1;
-    return done;
-  };
 
   // ---- phase 1
   {
-    int cur = 0;                                           // the (relative) unit that acc holds
-    for (int i = 0; ok && i < n1; i += len1) {
-      const int n = min(len1, n1 - i);
-      ok = wait_full();
-      if (!ok) break;
-      const uint8_t* sb = smem + slot * kMoeStage;
-      if (warp < n) {
-        const int u = (i + warp) / ipu1, pr = (i + warp) % ipu1;
-        while (cur < u) flush(cur++, 2);
-        const int x = (u1a + u) / P, first = l_first[x], cnt = l_first[x + 1] - first;
-        auto item = [&](auto mt) {
-          constexpr int MT = decltype(mt)::value;
-          const __half* xr[MT];
+    float acc[BL][2][MTT][4] = {};
+    // this warp's sums of a tile become its record
+    auto record = [&](float (&v)[MTT][4], int half, int cnt) {
+      float* p = rec_of(warp, half);
 #pragma unroll
-          for (int j = 0; j < MT; ++j)
-            xr[j] = a.x + static_cast<size_t>(l_token[first + min(8 * j + r, cnt - 1)]) * a.K + pr * 256 + 16 * t;
+      for (int m = 0; m < MTT; ++m)
+        if (8 * m < cnt)
 #pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            if (2 * pr + gg >= G1) break;
-            uint4 xv[2][MT][2];
+          for (int c = 0; c < 4; ++c) p[(8 * m + 2 * t + (c & 1)) * 20 + r + 8 * (c >> 1)] = v[m][c];
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
+      for (int m = 0; m < MTT; ++m)
 #pragma unroll
-              for (int j = 0; j < MT; ++j) {
-                xv[kk][j][0] = __ldg(reinterpret_cast<const uint4*>(xr[j] + gg * 128 + kk * 64));
-                xv[kk][j][1] = __ldg(reinterpret_cast<const uint4*>(xr[j] + gg * 128 + kk * 64 + 8));
+        for (int c = 0; c < 4; ++c) v[m][c] = 0.0f;
+    };
+    const int pl = warp % k1.wide, sub = warp / k1.wide;
+    for (int u = u1a; ok && u < u1b;) {
+      const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
+      const int first = l_first[x], cnt = l_first[x + 1] - first;
+      auto row_of = [&](int col) { return a.x + static_cast<size_t>(l_token[first + col]) * a.K; };
+      const __half* row8 = row_of(min(r, cnt - 1));
+      // `many`: more than 8 tokens (separate code, so that its fragments and f do not share registers)
+      auto expert = [&](auto many) {
+        constexpr bool kMany = decltype(many)::value;
+        MoeFrag f;
+        if (k1.strips == 1) {
+          for (int j0 = ja; ok && j0 < jb; j0 += BL) {
+            const int nb = min(BL, jb - j0);
+            for (int c = 0; ok && c < k1.chunks; ++c) {
+              const int pr = c * k1.len + pl;
+              const bool live = pl < min(k1.len, k1.Q - c * k1.len);
+              if (!kMany && live && (k1.chunks > 1 || j0 == ja)) {   // one chunk: they last for the expert
+                load_frag(f, row8, pr, G1);
+                sum_frag(f);
               }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int it = warp + h * (kMoeStageItems / 2);
-              const uint8_t* cb = sb + it * kPairCodeBytes + gg * 1024 + lane * 16;
-              const uint4 w0 = *reinterpret_cast<const uint4*>(cb);
-              const uint4 w1 = *reinterpret_cast<const uint4*>(cb + 512);
-              const uint32_t sv = *reinterpret_cast<const uint32_t*>(sb + kMoeOffS + it * kPairScaleBytes + gg * 32 + r * 4);
-              const uint32_t zz = sb[kMoeOffZ + it * kPairZeroBytes + gg * 8 + r];
-              gemv_group<MT>(reinterpret_cast<float(&)[MT][4]>(acc[h]), w0, w1, xv, sv, zz);
+              for (int b = 0; b < 2 * BL; ++b) {
+                if (b >= 2 * nb || !ok) break;
+                ok = take();
+                if (!ok) break;
+                if (live) {
+                  if constexpr (kMany) pair_many(acc[b >> 1][b & 1], pl, pr, G1, cnt, row_of);
+                  else pair8(acc[b >> 1][b & 1][0], f, pl);
+                }
+                release();
+                if (c == k1.chunks - 1) {
+                  if ((b & 1) == 0) ok = rec_ready();
+                  if (!ok) break;
+                  record(acc[b >> 1][b & 1], b & 1, cnt);
+                  if (b & 1) rec_done();
+                }
+              }
+            }
+          }
+        } else {
+          const int half = k1.strips / 2, i = sub % half;
+          if (!kMany && pl < k1.Q) {
+            load_frag(f, row8, pl, G1);
+            sum_frag(f);
+          }
+          for (int j0 = ja; ok && j0 < jb; j0 += half) {
+            ok = take();
+            if (!ok) break;
+            if (pl < k1.Q && j0 + i < jb) {
+              if constexpr (kMany) pair_many(acc[0][0], sub * k1.Q + pl, pl, G1, cnt, row_of);
+              else pair8(acc[0][0][0], f, sub * k1.Q + pl);
+            }
+            release();
+            ok = rec_ready();
+            if (!ok) break;
+            record(acc[0][0], 0, cnt);
+            rec_done();
+          }
+        }
+      };
+      if (MTT == 1 || cnt <= 8) expert(std::false_type{});
+      else expert(std::bool_constant<(MTT > 1)>{});
+      u += jb - ja;
+    }
+  }
+
+  ok = ok && warp_wait(go, 0);
+
+  // ---- phase 2: an expert's sums are added to its tokens' places in the warp's record
+  {
+    float acc[BL][MTT][4] = {};
+    const int pl = warp % k2.wide, sub = warp / k2.wide;
+    for (int t0 = u2a; ok && t0 < u2b; t0 += BL) {
+      const int nb = min(BL, u2b - t0);
+      ok = rec_ready();
+      if (!ok) break;
+      for (int b = 0; b < nb; ++b)
+        for (int i = lane; i < a.T * 20; i += 32) rec_of(warp, b)[i] = 0.0f;
+      __syncwarp();
+      for (int x0 = 0; ok && x0 < A; x0 += k2.strips) {
+        const int x = x0 + sub;
+        const bool mine = x < A;
+        const int first = mine ? l_first[x] : 0, cnt = mine ? l_first[x + 1] - first : 0;
+        auto row_of = [&](int col) { return a.h + static_cast<size_t>(first + col) * a.I; };
+        const __half* row8 = row_of(max(0, min(r, cnt - 1)));
+        auto expert = [&](auto many) {
+          constexpr bool kMany = decltype(many)::value;
+          for (int c = 0; ok && c < k2.chunks; ++c) {
+            const int n = min(k2.len, k2.Q - c * k2.len), pr = c * k2.len + pl;
+            const bool live = mine && pl < n;
+            MoeFrag f;
+            if (!kMany && live) {
+              load_frag(f, row8, pr, G2);
+              sum_frag(f);
+            }
+#pragma unroll
+            for (int b = 0; b < BL; ++b) {
+              if (b >= nb || !ok) break;
+              ok = take();
+              if (!ok) break;
+              if (live) {
+                if constexpr (kMany) pair_many(acc[b], sub * n + pl, pr, G2, cnt, row_of);
+                else pair8(acc[b][0], f, sub * n + pl);
+              }
+              release();
             }
           }
         };
-        if (MTT == 1 || cnt <= 8) item(std::integral_constant<int, 1>{});
-        else if (MTT == 2 || cnt <= 16) item(std::integral_constant<int, MTT < 2 ? 1 : 2>{});
-        else item(std::integral_constant<int, MTT>{});
-      }
-      release();
-      const int done0 = i / ipu1, done1 = (i + n) / ipu1;  // units that end within this stage
-      if (done1 > done0) {
-        while (cur < done1) flush(cur++, 2);
-        ok = consumer_sync();
+        if (MTT == 1 || cnt <= 8) expert(std::false_type{});
+        else expert(std::bool_constant<(MTT > 1)>{});
         if (!ok) break;
-        for (int v = done0; v < done1; ++v) {
-          const int x = (u1a + v) / P, j = (u1a + v) - x * P;
-          const int first = l_first[x], cnt = l_first[x + 1] - first;
-          for (int q = threadIdx.x; q < 16 * cnt; q += 32 * kMoeCW) {
-            const int row = q & 15, col = q >> 4;
-            if (!AWQ_CHECK(first + col < n_assign && 16 * j + row < a.I)) continue;
-            float hv = silu_mul(sum_of(v, 0, col, row), sum_of(v, 1, col, row)) * l_p[first + col];
-            if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + 16 * j + row));
-            a.h[static_cast<size_t>(first + col) * a.I + 16 * j + row] = __float2half_rn(hv);
+        if (mine && pl < k2.len) {
+#pragma unroll
+          for (int b = 0; b < BL; ++b) {
+            if (b >= nb) break;
+            float* p = rec_of(warp, b);
+#pragma unroll
+            for (int m = 0; m < MTT; ++m)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int col = 8 * m + 2 * t + c;
+                if (col < cnt) {
+                  float* pt = p + l_token[first + col] * 20 + r;
+                  pt[0] += acc[b][m][c];
+                  pt[8] += acc[b][m][c + 2];
+                }
+                acc[b][m][c] = acc[b][m][c + 2] = 0.0f;
+              }
           }
         }
       }
-    }
-  }
-
-  // ---- grid-wide barrier: every CTA's h is written (release) and visible (acquire)
-  __threadfence();
-  ok = ok && consumer_sync();
-  if (ok && threadIdx.x == 0) {
-    unsigned v;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(a.barrier) : "memory");
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.barrier) : "memory");
-      if (v >= gridDim.x || *s_abort) break;
-      if (globaltimer_ns() - t0 > budget) {
-        *s_abort = 1;
-        atomicOr(&g_dev_status, kDevStatusTimeout);
-        break;
-      }
-    }
-  }
-  ok = ok && consumer_sync() && *s_abort == 0;
-
-  // ---- phase 2
-  {
-    int cur = 0;
-    clear();
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int i = 0; ok && i < n2; i += len2) {
-      const int n = min(len2, n2 - i);
-      ok = wait_full();
-      if (!ok) break;
-      const uint8_t* sb = smem + slot * kMoeStage;
-      for (int it = warp; it < n; it += kMoeCW) {
-        const int u = (i + it) / ipu2, q = (i + it) % ipu2;
-        while (cur < u) flush(cur++, 1);
-        const int x = q / Q2, pr = q - x * Q2;
-        const __half* hr[MTT];
-        bool mine[MTT][2];                                 // whether this lane's two columns chose the expert
-#pragma unroll
-        for (int j = 0; j < MTT; ++j) {
-          const int s = 8 * j + r < a.T ? l_map[x * a.T + 8 * j + r] : -1;
-          hr[j] = s >= 0 ? a.h + static_cast<size_t>(s) * a.I + pr * 256 + 16 * t : nullptr;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) mine[j][c] = 8 * j + 2 * t + c < a.T && l_map[x * a.T + 8 * j + 2 * t + c] >= 0;
-        }
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          if (2 * pr + gg >= G2) break;
-          uint4 xv[2][MTT][2];
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int j = 0; j < MTT; ++j) {
-              xv[kk][j][0] = hr[j] != nullptr ? ld_coherent_v4(hr[j] + gg * 128 + kk * 64) : zero;
-              xv[kk][j][1] = hr[j] != nullptr ? ld_coherent_v4(hr[j] + gg * 128 + kk * 64 + 8) : zero;
-            }
-          const uint8_t* cb = sb + it * kPairCodeBytes + gg * 1024 + lane * 16;
-          const uint4 w0 = *reinterpret_cast<const uint4*>(cb);
-          const uint4 w1 = *reinterpret_cast<const uint4*>(cb + 512);
-          const uint32_t sv = *reinterpret_cast<const uint32_t*>(sb + kMoeOffS + it * kPairScaleBytes + gg * 32 + r * 4);
-          const uint32_t zz = sb[kMoeOffZ + it * kPairZeroBytes + gg * 8 + r];
-          float g[MTT][4] = {};
-          gemv_group<MTT>(g, w0, w1, xv, sv, zz);
-#pragma unroll
-          for (int j = 0; j < MTT; ++j)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (mine[j][c & 1]) acc[0][j][c] += g[j][c];
-        }
-      }
-      release();
-      const int done0 = i / ipu2, done1 = (i + n) / ipu2;
-      if (done1 > done0) {
-        while (cur < done1) flush(cur++, 1);
-        ok = consumer_sync();
-        if (!ok) break;
-        for (int v = done0; v < done1; ++v)
-          for (int q = threadIdx.x; q < 16 * a.T; q += 32 * kMoeCW) {
-            const int row = q & 15, col = q >> 4;
-            if (!AWQ_CHECK(16 * (u2a + v) + row < a.K)) continue;
-            a.y[static_cast<size_t>(col) * a.K + 16 * (u2a + v) + row] = __float2half_rn(sum_of(v, 0, col, row));
-          }
-      }
+      if (ok) rec_done();
     }
   }
 }
