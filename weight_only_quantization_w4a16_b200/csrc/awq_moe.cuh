@@ -204,6 +204,29 @@ struct MoeCut {
   }
 };
 
+// acc += S (sum x q) - S z (sum x) for the lane's four sums of one group (columns 2t, 2t+1 of rows r
+// and r+8), two columns to an instruction. tq carries 2^-24 (rows r) and 2^-20 (rows r+8).
+__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;"
+      : "+l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+}
+__device__ __forceinline__ void moe_scale(float (&acc)[4], const float (&tq)[4], const float (&xs)[2], uint32_t sv, uint32_t zz) {
+  const float2 sf = half2_bits_to_float2(sv);
+  const float s_lo = sf.x * 16777216.0f, s_hi = sf.y * 1048576.0f;   // 2^24 and 2^20: exact
+  const float z_lo = -sf.x * small_uint_to_float(zz & 0xFu), z_hi = -sf.y * small_uint_to_float(zz >> 4);
+  float2 lo = make_float2(acc[0], acc[1]), hi = make_float2(acc[2], acc[3]);
+  const float2 x2 = make_float2(xs[0], xs[1]);
+  fma2(lo, make_float2(s_lo, s_lo), make_float2(tq[0], tq[1]));
+  fma2(hi, make_float2(s_hi, s_hi), make_float2(tq[2], tq[3]));
+  fma2(lo, make_float2(z_lo, z_lo), x2);
+  fma2(hi, make_float2(z_hi, z_hi), x2);
+  acc[0] = lo.x;
+  acc[1] = lo.y;
+  acc[2] = hi.x;
+  acc[3] = hi.y;
+}
+
 // Sums of the activation fragments over a group, by an MMA whose A operand is all ones: lane (r, t)
 // gets those of its accumulator columns 2t and 2t+1.
 template <int MT>
@@ -240,7 +263,7 @@ __device__ __forceinline__ void moe_group(float (&acc)[MT][4], const uint4& c0, 
 #pragma unroll
     for (int s4 = 0; s4 < 4; ++s4) {
       const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
-      const uint32_t q8 = __umulhi(q, 1u << 24);   // q >> 8 on the multiply pipe
+      const uint32_t q8 = q >> 8;
       const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
@@ -251,16 +274,8 @@ __device__ __forceinline__ void moe_group(float (&acc)[MT][4], const uint4& c0, 
       }
     }
   }
-  const float2 sf = half2_bits_to_float2(sv);
-  const float s_lo = sf.x * 16777216.0f, s_hi = sf.y * 1048576.0f;   // 2^24 and 2^20: exact
-  const float z_lo = -sf.x * small_uint_to_float(zz & 0xFu), z_hi = -sf.y * small_uint_to_float(zz >> 4);
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    acc[j][0] += fmaf(s_lo, tq[j][0], z_lo * xs[j][0]);
-    acc[j][1] += fmaf(s_lo, tq[j][1], z_lo * xs[j][1]);
-    acc[j][2] += fmaf(s_hi, tq[j][2], z_hi * xs[j][0]);
-    acc[j][3] += fmaf(s_hi, tq[j][3], z_hi * xs[j][1]);
-  }
+  for (int j = 0; j < MT; ++j) moe_scale(acc[j], tq[j], xs[j], sv, zz);
 }
 
 // The activation fragments of one group pair for one 8-token tile, and their sums per group.
@@ -281,7 +296,7 @@ __device__ __forceinline__ void moe_pair(float (&acc)[4], const uint4 (&w)[2][2]
       for (int g = 0; g < 2; ++g) {
         const uint4& wv = w[g][kk];
         const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
-        const uint32_t q8 = __umulhi(q, 1u << 24);   // q >> 8 on the multiply pipe
+        const uint32_t q8 = q >> 8;
         const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
         const uint4& xq = f.v[g][kk][s4 >> 1];
         const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
@@ -289,15 +304,7 @@ __device__ __forceinline__ void moe_pair(float (&acc)[4], const uint4 (&w)[2][2]
         else mma_m16n8k16_f32(tq[g], a, b0, b1);
       }
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const float2 sf = half2_bits_to_float2(sv[g]);
-    const float s_lo = sf.x * 16777216.0f, s_hi = sf.y * 1048576.0f;   // 2^24 and 2^20: exact
-    const float z_lo = -sf.x * small_uint_to_float(zz[g] & 0xFu), z_hi = -sf.y * small_uint_to_float(zz[g] >> 4);
-    acc[0] += fmaf(s_lo, tq[g][0], z_lo * f.s[g][0]);
-    acc[1] += fmaf(s_lo, tq[g][1], z_lo * f.s[g][1]);
-    acc[2] += fmaf(s_hi, tq[g][2], z_hi * f.s[g][0]);
-    acc[3] += fmaf(s_hi, tq[g][3], z_hi * f.s[g][1]);
-  }
+  for (int g = 0; g < 2; ++g) moe_scale(acc, tq[g], f.s[g], sv[g], zz[g]);
 }
 
 // Bytes of the routing lists: expert counts, active experts, first slots (+1), assignment experts,
