@@ -156,10 +156,33 @@ def test_two_streams_at_once():
             with torch.cuda.stream(s):
                 out.append((case, layer(x)))
     torch.cuda.synchronize()
+    assert lib().awq_poll_device_status() == lib().AWQ_OK
     for case, y in out[-4:]:
         case.check(y, what="two streams")
     for (_, a), (_, b) in zip(out[::2], out[2::2]):
         assert torch.equal(a, b)
+
+
+def test_calls_back_to_back_with_early_launching_neighbours():
+    """Calls queued without a wait between them, next to kernels that launch their successors early: the
+    experts kernel's grid-wide barrier completes every time (the status word records a wait that ran out)."""
+    torch, P = torch_mod(), lib()
+    c, d = Case(1, 8, 2, 1024, 1024), Case(24, 16, 2, 512, 1024)
+    lc, ld = c.layer(), d.layer()
+    xc, xd = dev(c.x), dev(d.x)
+    ones = torch.ones(1024, device="cuda")
+    torch.cuda.synchronize()
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    out = []
+    for i in range(40):
+        a = P.awq_scale_activations(xc, ones)
+        out.append((lc(a), ld(xd)))
+        if i % 4 == 0:
+            lc(a)
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    c.check(out[-1][0])
+    d.check(out[-1][1])
+    assert all(torch.equal(a, out[0][0]) and torch.equal(b, out[0][1]) for a, b in out)
 
 
 def test_from_float_and_a_whole_block():

@@ -156,7 +156,8 @@ awq_status_t make_weight_maps(CUtensorMap* qm, CUtensorMap* sm, CUtensorMap* zm,
 // Every kernel is launched with programmatic stream serialization (PDL): it may start while the
 // previous kernel of the stream drains, runs its prologue, and waits (griddepcontrol.wait) before
 // touching data a predecessor may write. A cluster shape with x > 0 adds a thread-block cluster.
-// `cooperative`: all CTAs are resident at once or the launch waits (kernels with a grid-wide barrier).
+// `cooperative`: all CTAs are resident at once or the launch waits (kernels with a grid-wide barrier),
+// without programmatic serialization.
 template <typename... KArgs, typename... Args>
 awq_status_t launch_attr(void (*kernel)(KArgs...), dim3 grid, dim3 block, dim3 cluster, bool cooperative, size_t smem,
                          cudaStream_t stream, Args... args) {
@@ -165,11 +166,13 @@ awq_status_t launch_attr(void (*kernel)(KArgs...), dim3 grid, dim3 block, dim3 c
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[3];
+  cudaLaunchAttribute attr[2];
   int na = 0;
-  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[na].val.programmaticStreamSerializationAllowed = 1;
-  ++na;
+  if (!cooperative) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
   if (cluster.x > 0) {
     attr[na].id = cudaLaunchAttributeClusterDimension;
     attr[na].val.clusterDim.x = cluster.x;
@@ -712,17 +715,15 @@ inline bool search_shape_ok(int M, int N, int K) {
 
 
 // --------------------------------------------------------------------------- mixture of experts
-// Workspace: the grid barrier, the routing and the intermediate h, each piece 256-byte aligned.
+// Workspace: the router's logits and the intermediate h, each piece 256-byte aligned.
 struct MoeWs {
-  size_t barrier, ids, p, h, total;
+  size_t logits, h, total;
 };
-MoeWs moe_ws(int T, int I, int top) {
+MoeWs moe_ws(int T, int E, int I, int top) {
   MoeWs w{};
-  const size_t n = static_cast<size_t>(T) * top;
-  size_t o = 256;
-  w.ids = o; o = align256(o + n * 4);
-  w.p = o; o = align256(o + n * 4);
-  w.h = o; o = align256(o + n * I * 2);
+  size_t o = 0;
+  w.logits = o; o = align256(o + static_cast<size_t>(T) * E * 4);
+  w.h = o; o = align256(o + static_cast<size_t>(T) * top * I * 2);
   w.total = o;
   return w;
 }
@@ -730,16 +731,6 @@ inline bool moe_shape_ok(int T, int E, int K, int I, int top) {
   return T >= 1 && T <= kMoeMaxTokens && E >= 1 && E <= kMoeMaxExperts && top >= 1 && top <= kMoeMaxTopK && top <= E &&
          K >= kGroup && K % kGroup == 0 && I >= kGroup && I % kGroup == 0 && I <= kMaxRows / 2 && rows_ok(2 * I, K) &&
          rows_ok(K, I);
-}
-
-template <int MT>
-awq_status_t launch_moe_experts(const MoeArgs& a, int dev, int num_sms, cudaStream_t stream) {
-  auto kernel = awq_moe_experts_kernel<MT>;
-  static std::atomic<uint64_t> smem_done{0};
-  const awq_status_t st = ensure_smem(kernel, 227 * 1024, dev, smem_done);
-  if (st != AWQ_OK) return st;
-  return launch_attr(kernel, dim3(static_cast<unsigned>(num_sms), 1, 1), dim3(kMoeThreads, 1, 1), dim3(0, 0, 0), true,
-                     static_cast<size_t>(moe_smem_bytes<MT>(a.T, a.E, a.top)), stream, a);
 }
 
 // Scratch of awq_search_alpha_noalloc: a file-scope device array, so that callers which cannot
@@ -1116,7 +1107,7 @@ awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, cons
 }
 
 size_t awq_moe_workspace_bytes(int T, int E, int K, int I, int top_k) {
-  return moe_shape_ok(T, E, K, I, top_k) ? moe_ws(T, I, top_k).total : 0;
+  return moe_shape_ok(T, E, K, I, top_k) ? moe_ws(T, E, I, top_k).total : 0;
 }
 
 awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint32_t* gate_up_qweight,
@@ -1128,7 +1119,7 @@ awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint
       !down_zeros || !y || !workspace)
     return AWQ_ERR_INVALID_ARG;
   if (!moe_shape_ok(T, E, K, I, top_k)) return AWQ_ERR_INVALID_ARG;
-  const MoeWs w = moe_ws(T, I, top_k);
+  const MoeWs w = moe_ws(T, E, I, top_k);
   if (workspace_bytes < w.total) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(router) || !aligned16(gate_up_qweight) || !aligned16(gate_up_scales) ||
       !aligned16(gate_up_zeros) || !aligned16(down_qweight) || !aligned16(down_scales) || !aligned16(down_zeros) ||
@@ -1150,19 +1141,17 @@ awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint
   a.gu_pairs = tile_pairs(2 * I, K);
   a.dn_pairs = tile_pairs(K, I);
   a.h_scale = h_scale;
-  a.ids = reinterpret_cast<const int*>(ws + w.ids);
-  a.p = reinterpret_cast<const float*>(ws + w.p);
+  a.router = reinterpret_cast<const __half*>(router);
+  a.logits = reinterpret_cast<float*>(ws + w.logits);
   a.h = reinterpret_cast<__half*>(ws + w.h);
   a.y = reinterpret_cast<__half*>(y);
-  a.barrier = reinterpret_cast<unsigned*>(ws + w.barrier);
   a.T = T; a.E = E; a.K = K; a.I = I; a.top = top_k;
-  const MoeRouteArgs ra = {a.x, reinterpret_cast<const __half*>(router), reinterpret_cast<int*>(ws + w.ids),
-                           reinterpret_cast<float*>(ws + w.p), a.barrier, T, E, K, top_k, renormalize != 0};
-  st = launch_ex(awq_moe_route_kernel, dim3(kRouteCluster * ceil_div(T, kRouteTokens), 1, 1), dim3(32 * kRouteWarps, 1, 1),
-                 dim3(0, 0, 0), 0, cs, ra);
-  if (st != AWQ_OK) return st;
-  return T <= 8 ? launch_moe_experts<1>(a, dev, sms, cs) : T <= 16 ? launch_moe_experts<2>(a, dev, sms, cs)
-                                                                   : launch_moe_experts<4>(a, dev, sms, cs);
+  a.renorm = renormalize != 0;
+  a.bufs = moe_bufs(T);
+  static std::atomic<uint64_t> smem_done{0};
+  if ((st = ensure_smem(awq_moe_kernel, 227 * 1024, dev, smem_done)) != AWQ_OK) return st;
+  return launch_attr(awq_moe_kernel, dim3(static_cast<unsigned>(sms), 1, 1), dim3(kMoeThreads, 1, 1), dim3(0, 0, 0), true,
+                     static_cast<size_t>(moe_smem_bytes(T, top_k)), cs, a);
 }
 
 awq_status_t awq_poll_device_status(awq_stream_t stream) {

@@ -1,5 +1,5 @@
 // awq_moe.cuh — a whole mixture-of-experts layer for a few tokens (T <= 32), experts in packed
-// 4-bit weights, in two kernels.
+// 4-bit weights, in one kernel.
 //
 //   l_te = x_t . Wr_e              the top_k experts of token t by l (ties: lowest index)
 //   p_te = exp(l_te - max) / sum   the sum over all experts, or over the chosen ones (renormalize)
@@ -7,192 +7,73 @@
 //   y_t  = sum over the chosen e of h . Wd_e^T
 //
 // The layer is bound by the packed weights of the experts that are chosen at all (0.52 bytes per
-// weight, each read once whatever the number of its tokens).
+// weight). One CTA per SM, launched cooperatively, in three phases with a grid-wide barrier between:
+//   0  the router's logits, a CTA per expert and 8 tokens; after the barrier every CTA picks all
+//      tokens' experts itself and sorts the choices into blocks of at most 8 tokens of one expert;
+//   1  h for every unit (block, 16 gate rows and their 16 up rows);
+//   2  y for every 16-row output tile, summed over the blocks.
+// An expert with more than 8 tokens has several blocks, whose weights come from L2 after the first:
+// each block's activation fragments then fit a warp's registers.
 //
-// awq_moe_route_kernel: clusters of 8 CTAs, 4 tokens each; the CTAs split the experts, rank 0
-// gathers the logits through distributed shared memory and one warp per token picks its experts.
+// Per CTA: a producer lane streams both phases' packed weights through one ring of shared memory
+// without waiting for the barrier, so phase 2's first weights arrive while phase 1 ends. A stage holds
+// 16 (tile, group pair) items, one for each of the 16 consumer warps, which so split a tile's K. A
+// warp's activation fragments stay in registers while it walks along the tiles of a block. Each warp
+// leaves its sums of a tile in shared memory, and an epilogue warp adds them in warp order and applies
+// SiLU, the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding
+// (2^-12 of each term on average) is the one that unfused layers make between their calls.
 //
-// awq_moe_experts_kernel: one CTA per SM, launched cooperatively. Phase 1 computes h for every
-// (expert, 16 gate rows + their 16 up rows) unit, phase 2 the output tiles of 16 rows, summed over
-// the experts; a grid-wide barrier lies between. A producer lane streams both phases' packed weights
-// through one ring without waiting for the barrier, so phase 2's first weights arrive while phase 1
-// ends. The consumer warps split a unit's group pairs and use the exact integer dequantization and
-// warp MMAs of the decode kernel; activations are read through L1, the columns of an MMA being the
-// expert's own tokens. Phase 2 adds an expert's columns to its tokens' places in the warp's record.
-// h carries p: its fp16 rounding (2^-12 of each term on average) is the one the unfused layers make
-// between their calls.
-// Partial sums of the warps are added in warp order: results repeat bit for bit.
+// The kernel neither starts before its predecessor has ended nor lets its successor start early: CTAs
+// that wait for it could otherwise hold the registers that its own last CTAs need, and the barrier
+// would never be complete.
 #pragma once
 
-#include <cooperative_groups.h>
-
-#include <type_traits>
-
 #include "awq_common.cuh"
-#include "awq_gemv.cuh"
+#include "awq_gemm.cuh"
 
 namespace awq {
 
 constexpr int kMoeMaxTokens = 32;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
-constexpr int kRouteCluster = 8;
-constexpr int kRouteTokens = 4;      // tokens per cluster
-constexpr int kRouteWarps = 8;
 
-// ---------------------------------------------------------------------------- routing
-struct MoeRouteArgs {
-  const __half* x;        // [T, K]
-  const __half* router;   // [E, K]
-  int* ids;               // [T, top]
-  float* p;               // [T, top]
-  unsigned* barrier;      // zeroed for the experts kernel
-  int T, E, K, top, renorm;
-};
-
-__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(32 * kRouteWarps)
-    awq_moe_route_kernel(const MoeRouteArgs a) {
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
-  __shared__ float s_logits[kRouteTokens][kMoeMaxExperts];                                   // rank 0's is used
-  __shared__ float s_part[kRouteWarps][kMoeMaxExperts / kRouteCluster][kRouteTokens];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int rank = static_cast<int>(cluster.block_rank());
-  const int t0 = static_cast<int>(blockIdx.x) / kRouteCluster * kRouteTokens;
-  const int nt = min(kRouteTokens, a.T - t0);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 1 && threadIdx.x == 0) *a.barrier = 0u;
-  // this CTA's experts; with few of them several warps split K
-  const int epc = ceil_div(a.E, kRouteCluster), e0 = rank * epc;
-  const int wpe = epc == 1 ? 8 : epc == 2 ? 4 : epc <= 4 ? 2 : 1;
-  const int part = warp % wpe;
-  const __half* xr[kRouteTokens];
-#pragma unroll
-  for (int t = 0; t < kRouteTokens; ++t) xr[t] = a.x + static_cast<size_t>(t0 + min(t, nt - 1)) * a.K;
-  for (int le = warp / wpe; le < epc && e0 + le < a.E; le += kRouteWarps / wpe) {
-    const __half* wr = a.router + static_cast<size_t>(e0 + le) * a.K;
-    float acc[kRouteTokens] = {};
-#pragma unroll 4
-    for (int c = part * 32 + lane; c < a.K / 8; c += 32 * wpe) {
-      const uint4 wv = __ldg(reinterpret_cast<const uint4*>(wr + c * 8));
-      const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-      for (int t = 0; t < kRouteTokens; ++t) {
-        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(xr[t] + c * 8));
-        const uint32_t x4[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 wf = half2_bits_to_float2(w4[j]), xf = half2_bits_to_float2(x4[j]);
-          acc[t] = fmaf(wf.x, xf.x, acc[t]);
-          acc[t] = fmaf(wf.y, xf.y, acc[t]);
-        }
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kRouteTokens; ++t) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
-      if (lane == 0) s_part[part][le][t] = acc[t];
-    }
-  }
-  __syncthreads();
-  float* dst = cluster.map_shared_rank(&s_logits[0][0], 0);
-  for (int i = threadIdx.x; i < epc * kRouteTokens; i += blockDim.x) {
-    const int le = i / kRouteTokens, t = i % kRouteTokens;
-    if (e0 + le >= a.E) continue;
-    float v = 0.0f;
-    for (int q = 0; q < wpe; ++q) v += s_part[q][le][t];
-    dst[t * kMoeMaxExperts + e0 + le] = v;
-  }
-  cluster.sync();
-  if (rank != 0 || warp >= nt) return;
-  // one warp per token. Keys order by (logit, lowest index first); a NaN orders below every number and
-  // a chosen expert's key is 0, so top_k distinct experts are found whatever the logits are.
-  constexpr int kPer = kMoeMaxExperts / 32;
-  unsigned long long key[kPer];
-  float best = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = 0;
-    if (e < a.E) {
-      const float v = s_logits[warp][e];
-      best = fmaxf(best, v);
-      const uint32_t b = __float_as_uint(v);
-      const uint32_t ord = v != v ? 0u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-      key[i] = (static_cast<unsigned long long>(ord) << 32) | static_cast<uint32_t>(~e);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-  float total = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (i * 32 + lane < a.E) total += expf(s_logits[warp][i * 32 + lane] - best);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-  float mine = 0.0f, chosen = 0.0f;   // lane k: the numerator of the k-th choice
-  int mine_id = 0;
-  for (int k = 0; k < a.top; ++k) {
-    unsigned long long m = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) m = key[i] > m ? key[i] : m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xFFFFFFFFu, m, o);
-      m = other > m ? other : m;
-    }
-    const int e = static_cast<int>(~static_cast<uint32_t>(m));
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (key[i] == m) key[i] = 0;
-    const float v = expf(s_logits[warp][e] - best);
-    chosen += v;
-    if (lane == k) { mine = v; mine_id = e; }
-  }
-  if (lane < a.top) {
-    a.ids[(t0 + warp) * a.top + lane] = mine_id;
-    a.p[(t0 + warp) * a.top + lane] = __fdiv_rn(mine, a.renorm ? chosen : total);
-  }
-}
-
-// ---------------------------------------------------------------------------- experts
 struct MoeArgs {
   const __half* x;                             // [T, K]
+  const __half* router;                        // [E, K]
   const uint8_t *gu_q, *gu_s, *gu_z;           // gate/up layers, packed layout v2, one after another
   const uint8_t *dn_q, *dn_s, *dn_z;           // down layers
   size_t gu_pairs, dn_pairs;                   // (tile, group pair) items of one expert's layer
   const float* h_scale;                        // [E, I] or null
-  const int* ids;                              // [T, top]
-  const float* p;
+  float* logits;                               // [T, E]
   __half* h;                                   // [T * top, I]
   __half* y;                                   // [T, K]
-  unsigned* barrier;
-  int T, E, K, I, top;
+  int T, E, K, I, top, renorm;
+  int bufs;                                    // record buffers
 };
 
 constexpr int kMoeCW = 16;                      // consumer warps
 constexpr int kMoeThreads = 32 * (kMoeCW + 2);  // + producer, + epilogue
+constexpr int kMoeStages = 4;
 constexpr int kMoeStageItems = 16;              // (tile, group pair) items per ring stage, one per consumer warp
 constexpr int kMoeOffS = kMoeStageItems * kPairCodeBytes;
 constexpr int kMoeOffZ = kMoeOffS + kMoeStageItems * kPairScaleBytes;
 constexpr int kMoeStage = kMoeOffZ + kMoeStageItems * kPairZeroBytes;   // 34048 bytes
 static_assert(kMoeStage % 128 == 0, "ring stages stay aligned");
 
-// MTT: 8-token tiles (T <= 8 MTT). A record is one warp's fp32 sums of one 16-row tile, [column][20]
-// (20: rows padded so that the fragment stores hit distinct banks).
-template <int MTT>
-struct MoeCfg {
-  static constexpr int kStages = MTT == 4 ? 3 : 4;
-  static constexpr int kBlock = MTT == 1 ? 2 : 1;       // tiles per warp that share activation fragments
-  static constexpr int kRec = 8 * MTT * 20;             // floats
-  static constexpr int kBufs = MTT == 4 ? 1 : 2;        // record buffers (two tiles each)
-  static constexpr int kRecBytes = kBufs * kMoeCW * 2 * kRec * 4;
-  static constexpr int kBars = 2 * kStages + 2 * kBufs + 1;
-};
+// A record is one warp's fp32 sums of one 16-row tile, [column][20] (20: rows padded so that the
+// fragment stores hit distinct banks): a block's 8 columns in phase 1, the T tokens in phase 2.
+// A buffer holds two tiles' records of every warp; two buffers while they leave room for the ring.
+__host__ __device__ inline int moe_rec_floats(int T) { return (T < 8 ? 8 : T) * 20; }
+__host__ __device__ inline int moe_bufs(int T) { return T <= 16 ? 2 : 1; }
+// Routing lists: the choices in (token, rank) order (expert, weight), whose place the blocks (expert,
+// first slot; one more) take; then by slot the token, weight and expert.
+__host__ __device__ inline int moe_list_ints(int T, int top) { return 5 * T * top + 1; }
+__host__ __device__ inline int moe_smem_bytes(int T, int top) {
+  return kMoeStages * kMoeStage + moe_bufs(T) * kMoeCW * 2 * moe_rec_floats(T) * 4 + (2 * kMoeStages + 5) * 8 + 8 +
+         moe_list_ints(T, top) * 4;
+}
 
-// How a strip (one tile of one expert, Q group pairs along its K) is cut into stages. Up to 8 pairs:
+// How a strip (one tile of one block, Q group pairs along its K) is cut into stages. Up to 8 pairs:
 // `strips` strips share a stage, `wide` warps each. More: `chunks` stages of up to `len` pairs.
 struct MoeCut {
   int Q, wide, strips, chunks, len;
@@ -203,6 +84,98 @@ struct MoeCut {
     len = (q + chunks - 1) / chunks;
   }
 };
+
+// Arrivals at the grid-wide barriers since the library was loaded. Every CTA of a launch arrives at
+// each barrier exactly once, also when it has given up a wait, so the count is a multiple of the grid
+// size between barriers. One counter is enough: a CTA takes more than half of an SM's shared memory
+// and the grid all SMs, so two launches never run at once, and none of a launch's CTAs ends before
+// all have arrived at its last barrier.
+__device__ unsigned long long g_moe_arrivals = 0;
+static_assert(kMoeStages * kMoeStage > 114 * 1024, "two of these CTAs must not fit one SM");
+
+__device__ __forceinline__ unsigned long long moe_arrive() {
+  unsigned long long old;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(&g_moe_arrivals) : "memory");
+  return old - old % gridDim.x + gridDim.x;    // the count at which the barrier is complete
+}
+__device__ __forceinline__ void moe_await(unsigned long long target, volatile int* abort, unsigned long long budget) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!*abort) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(&g_moe_arrivals) : "memory");
+    if (v >= target) return;
+    if (globaltimer_ns() - t0 > budget) {
+      *abort = 1;
+      atomicOr(&g_dev_status, kDevStatusTimeout);
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 ld_coherent_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// One warp picks a token's experts from its E <= 32 PER logits. `ord` orders the logits as integers; a
+// NaN is 1, below every number, and a chosen expert (or none) 0, so that `top` distinct experts are
+// found whatever the logits are.
+template <int PER>
+__device__ __forceinline__ void moe_pick(const float* logits, int E, int top, bool renorm, int* ids, float* p) {
+  const int lane = threadIdx.x & 31;
+  uint32_t ord[PER];
+  float l[PER], best = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    ord[i] = 0;
+    l[i] = -INFINITY;
+    if (e < E) {
+      asm volatile("ld.global.f32 %0, [%1];" : "=f"(l[i]) : "l"(logits + e));
+      const uint32_t b = __float_as_uint(l[i]);
+      ord[i] = l[i] != l[i] ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) best = fmaxf(best, l[i]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+  float total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    l[i] = expf(l[i] - best);
+    if (i * 32 + lane < E) total += l[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  float mine = 0.0f, chosen = 0.0f;            // lane k: the k-th choice
+  int mine_id = 0;
+  for (int k = 0; k < top; ++k) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = max(m, ord[i]);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    uint32_t e = 0xFFFFFFFFu;                  // the lowest index among the equal ones
+    float v = 0.0f;
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i)
+      if (ord[i] == m) {
+        e = i * 32 + lane;
+        v = l[i];
+      }
+    const uint32_t first = __reduce_min_sync(0xFFFFFFFFu, e);
+    v = __shfl_sync(0xFFFFFFFFu, v, first & 31);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane == static_cast<int>(first)) ord[i] = 0;
+    chosen += v;
+    if (lane == k) { mine = v; mine_id = static_cast<int>(first); }
+  }
+  if (lane < top) {
+    ids[lane] = mine_id;
+    p[lane] = __fdiv_rn(mine, renorm ? chosen : total);
+  }
+}
 
 // acc += S (sum x q) - S z (sum x) for the lane's four sums of one group (columns 2t, 2t+1 of rows r
 // and r+8), two columns to an instruction. tq carries 2^-24 (rows r) and 2^-20 (rows r+8).
@@ -227,64 +200,16 @@ __device__ __forceinline__ void moe_scale(float (&acc)[4], const float (&tq)[4],
   acc[3] = hi.y;
 }
 
-// Sums of the activation fragments over a group, by an MMA whose A operand is all ones: lane (r, t)
-// gets those of its accumulator columns 2t and 2t+1.
-template <int MT>
-__device__ __forceinline__ void moe_sums(float (&xs)[MT][2], const uint4 (&xv)[2][MT][2]) {
-  const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    float d[4];
-    mma_m16n8k16_f32_zero(d, ones, xv[0][j][0].x, xv[0][j][0].y);
-    mma_m16n8k16_f32(d, ones, xv[0][j][0].z, xv[0][j][0].w);
-    mma_m16n8k16_f32(d, ones, xv[0][j][1].x, xv[0][j][1].y);
-    mma_m16n8k16_f32(d, ones, xv[0][j][1].z, xv[0][j][1].w);
-    mma_m16n8k16_f32(d, ones, xv[1][j][0].x, xv[1][j][0].y);
-    mma_m16n8k16_f32(d, ones, xv[1][j][0].z, xv[1][j][0].w);
-    mma_m16n8k16_f32(d, ones, xv[1][j][1].x, xv[1][j][1].y);
-    mma_m16n8k16_f32(d, ones, xv[1][j][1].z, xv[1][j][1].w);
-    xs[j][0] = d[0];
-    xs[j][1] = d[1];
-  }
-}
-
-// acc += S (sum x q - z sum x) for one group. A code pair masked out of its word is a pair of fp16
-// subnormals q 2^-24 (16 q 2^-24 in the odd nibbles, rows r+8): one AND makes an operand of the MMA,
-// whose products are exact. The zero point costs no instruction per code: it enters once per group
-// with the group's activation sum. 66 instructions per 2048 weights, where subtracting it from
-// every code pair takes about 130 and made the integer pipe the bound.
-template <int MT>
-__device__ __forceinline__ void moe_group(float (&acc)[MT][4], const uint4& c0, const uint4& c1,
-                                          const uint4 (&xv)[2][MT][2], const float (&xs)[MT][2], uint32_t sv, uint32_t zz) {
-  float tq[MT][4];
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-    const uint4& wv = kk ? c1 : c0;
-#pragma unroll
-    for (int s4 = 0; s4 < 4; ++s4) {
-      const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
-      const uint32_t q8 = q >> 8;
-      const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const uint4& xq = xv[kk][j][s4 >> 1];
-        const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
-        if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[j], a, b0, b1);
-        else mma_m16n8k16_f32(tq[j], a, b0, b1);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) moe_scale(acc[j], tq[j], xs[j], sv, zz);
-}
-
 // The activation fragments of one group pair for one 8-token tile, and their sums per group.
 struct MoeFrag {
   uint4 v[2][2][2];   // [group][64-k tile][half]
   float s[2][2];      // [group][column 2t, 2t+1]
 };
 
-// One group pair with at most 8 tokens: the two groups' MMA chains run side by side.
+// One group pair. A code pair masked out of its word is a pair of fp16 subnormals q 2^-24 (16 q 2^-24
+// in the odd nibbles, rows r+8): one AND makes an operand of the MMA, whose products are exact. The zero
+// point costs no instruction per code, it enters once per group with the group's activation sum. The
+// two groups' MMA chains run side by side.
 __device__ __forceinline__ void moe_pair(float (&acc)[4], const uint4 (&w)[2][2], const MoeFrag& f, const uint32_t (&sv)[2],
                                          const uint32_t (&zz)[2]) {
   float tq[2][4];
@@ -307,44 +232,25 @@ __device__ __forceinline__ void moe_pair(float (&acc)[4], const uint4 (&w)[2][2]
   for (int g = 0; g < 2; ++g) moe_scale(acc, tq[g], f.s[g], sv[g], zz[g]);
 }
 
-// Bytes of the routing lists: expert counts, active experts, first slots (+1), assignment experts,
-// slot tokens, slot weights.
-__host__ __device__ inline int moe_list_bytes(int T, int E, int top) {
-  const int n = T * top, act = n < E ? n : E;
-  return (E + 2 * act + 1 + 3 * n) * 4;
-}
-template <int MT>
-__host__ __device__ inline int moe_smem_bytes(int T, int E, int top) {
-  using C = MoeCfg<MT>;
-  return C::kStages * kMoeStage + C::kRecBytes + C::kBars * 8 + 8 + moe_list_bytes(T, E, top);
-}
-__device__ __forceinline__ uint4 ld_coherent_v4(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-template <int MTT>
-__global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const MoeArgs a) {
-  using C = MoeCfg<MTT>;
-  constexpr int S = C::kStages;
+__global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a) {
+  constexpr int S = kMoeStages;
   extern __shared__ __align__(128) uint8_t smem[];
+  const int rec_floats = moe_rec_floats(a.T);
   float* rec = reinterpret_cast<float*>(smem + S * kMoeStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kMoeStage + C::kRecBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(rec + a.bufs * kMoeCW * 2 * rec_floats);
   uint64_t* empty = full + S;
   uint64_t* rfull = empty + S;                 // record buffers
-  uint64_t* rempty = rfull + C::kBufs;
-  uint64_t* go = rempty + C::kBufs;            // phase 2 may read h
+  uint64_t* rempty = rfull + 2;
+  uint64_t* go = rempty + 2;                   // phase 2 may read h
   volatile int* s_abort = reinterpret_cast<volatile int*>(go + 1);
-  int* s_active = const_cast<int*>(s_abort) + 1;
   const int n_assign = a.T * a.top;
-  const int max_act = min(n_assign, a.E);
-  int* l_count = s_active + 1;                 // [E]: counts, then the active index
-  int* l_expert = l_count + a.E;               // [max_act]: expert of an active index
-  int* l_first = l_expert + max_act;           // [max_act + 1]: its first slot
-  int* l_ids = l_first + max_act + 1;          // [n_assign]
-  int* l_token = l_ids + n_assign;             // [n_assign]: token of a slot
-  float* l_p = reinterpret_cast<float*>(l_token + n_assign);   // [n_assign]: weight of a slot
+  int* l_ids = const_cast<int*>(s_abort) + 2;
+  float* l_pa = reinterpret_cast<float*>(l_ids + n_assign);
+  int* l_expert = l_ids;
+  int* l_first = l_ids + n_assign;
+  int* l_token = l_first + n_assign + 1;
+  float* l_p = reinterpret_cast<float*>(l_token + n_assign);
+  int* l_slot = reinterpret_cast<int*>(l_p + n_assign);        // expert of a slot, times two, + 1 where a block starts
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -352,7 +258,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kMoeCW);
     }
-    for (int b = 0; b < C::kBufs; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&rfull[b], kMoeCW);
       mbar_init(&rempty[b], 1);
     }
@@ -360,75 +266,110 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
     *s_abort = 0;
     mbar_fence_init();
   }
-  pdl_launch_dependents();
-  pdl_wait();
   const unsigned long long budget = g_wait_budget_ns;
+  const int c0 = blockIdx.x, nc = gridDim.x;
 
-  // ---- the experts that are chosen and their slots (token order)
-  for (int i = threadIdx.x; i < a.E; i += kMoeThreads) l_count[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n_assign; i += kMoeThreads) {
-    const int e = a.ids[i];
-    l_ids[i] = e;
-    atomicAdd(&l_count[e], 1);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int act = 0, slots = 0;
-    for (int b = 0; b < a.E; b += 32) {
-      const int e = b + lane, c = e < a.E ? l_count[e] : 0;
-      const uint32_t live = __ballot_sync(0xFFFFFFFFu, c > 0);
-      int before = c;
+  // ---- phase 0: logits of 8 tokens with one expert, the consumer warps splitting K
+  {
+    float* part = rec;                         // [2][kMoeCW][8]
+    const int tasks = a.E * ((a.T + 7) / 8);
+    for (int i = c0, it = 0; i < tasks; i += nc, it ^= 1) {
+      const int e = i % a.E, t0 = i / a.E * 8;
+      float acc[8] = {};
+      if (warp < kMoeCW) {
+        const __half* wr = a.router + static_cast<size_t>(e) * a.K;
+        for (int c = threadIdx.x; c < a.K / 8; c += 32 * kMoeCW) {
+          const uint4 wv = __ldg(reinterpret_cast<const uint4*>(wr + c * 8));
+          const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
-        if (lane >= o) before += v;
+          for (int t = 0; t < 8; ++t) {
+            if (t0 + t >= a.T) break;
+            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t0 + t) * a.K + c * 8));
+            const uint32_t x4[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 wf = half2_bits_to_float2(w4[j]), xf = half2_bits_to_float2(x4[j]);
+              acc[t] = fmaf(wf.x, xf.x, acc[t]);
+              acc[t] = fmaf(wf.y, xf.y, acc[t]);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (t0 + t >= a.T) break;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
+          if (lane == 0) part[(it * kMoeCW + warp) * 8 + t] = acc[t];
+        }
       }
-      const int all = __shfl_sync(0xFFFFFFFFu, before, 31);
-      const int idx = act + __popc(live & ((1u << lane) - 1));
-      if (c > 0) {
-        l_expert[idx] = e;
-        l_first[idx] = slots + before - c;
+      __syncthreads();
+      if (threadIdx.x < 8 && t0 + threadIdx.x < a.T) {
+        float v = 0.0f;
+        for (int w = 0; w < kMoeCW; ++w) v += part[(it * kMoeCW + w) * 8 + threadIdx.x];
+        a.logits[static_cast<size_t>(t0 + threadIdx.x) * a.E + e] = v;
       }
-      if (e < a.E) l_count[e] = idx;
-      act += __popc(live);
-      slots += all;
     }
-    if (lane == 0) {
-      l_first[act] = slots;
-      *s_active = act;
-    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) moe_await(moe_arrive(), s_abort, budget);
+    __syncthreads();
+  }
+
+  // ---- the choices, and the blocks: slots ordered by expert, then token
+  for (int t = warp; t < a.T; t += kMoeThreads / 32) {
+    const float* l = a.logits + static_cast<size_t>(t) * a.E;
+    int* ids = l_ids + t * a.top;
+    float* p = l_pa + t * a.top;
+    if (a.E <= 32) moe_pick<1>(l, a.E, a.top, a.renorm != 0, ids, p);
+    else if (a.E <= 128) moe_pick<4>(l, a.E, a.top, a.renorm != 0, ids, p);
+    else moe_pick<kMoeMaxExperts / 32>(l, a.E, a.top, a.renorm != 0, ids, p);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_assign; i += kMoeThreads) {
-    const int e = l_ids[i], idx = l_count[e];
-    int rank = 0;
-    for (int j = 0; j < i; ++j) rank += l_ids[j] == e;
-    const int slot = l_first[idx] + rank;
-    l_token[slot] = i / a.top;
-    l_p[slot] = a.p[i];
+    const int e = l_ids[i];
+    int rank = 0, first = 0;
+    for (int j = 0; j < n_assign; ++j) {
+      const int o = l_ids[j];
+      first += o < e;
+      rank += o == e && j < i;
+    }
+    l_token[first + rank] = i / a.top;
+    l_p[first + rank] = l_pa[i];
+    l_slot[first + rank] = 2 * e + (rank % 8 == 0);
   }
   __syncthreads();
+  int V = 0;                                   // blocks
+  for (int b = 0; b < n_assign; b += 32) {     // every warp counts, one writes
+    const int v = b + lane < n_assign ? l_slot[b + lane] : 0;
+    const uint32_t starts = __ballot_sync(0xFFFFFFFFu, v & 1);
+    if (warp == 0 && (v & 1)) {
+      const int idx = V + __popc(starts & ((1u << lane) - 1));
+      l_expert[idx] = v >> 1;
+      l_first[idx] = b + lane;
+    }
+    V += __popc(starts);
+  }
+  if (threadIdx.x == 0) l_first[V] = n_assign;
+  __syncthreads();
 
-  // ---- this CTA's work. Phase 1: units (active expert, 16-row gate tile and its up tile). Phase 2:
-  // 16-row output tiles, over all active experts. All roles walk the same stages in the same order.
-  const int A = *s_active, P = a.I / 16;
+  // ---- this CTA's work; all roles walk the same stages in the same order
+  const int P = a.I / 16;
   const int G1 = a.K / kGroup, G2 = a.I / kGroup;
   const MoeCut k1((G1 + 1) / 2), k2((G2 + 1) / 2);
-  const int c0 = blockIdx.x, nc = gridDim.x;
   auto share = [&](int units, int c) { return static_cast<int>(static_cast<long long>(units) * c / nc); };
-  const int u1a = share(A * P, c0), u1b = share(A * P, c0 + 1);
+  const int u1a = share(V * P, c0), u1b = share(V * P, c0 + 1);
   const int u2a = share(a.K / 16, c0), u2b = share(a.K / 16, c0 + 1);
-  constexpr int BL = C::kBlock;
   int slot = 0;
   uint32_t phase = 0;
   auto advance = [&]() {
     if (++slot == S) { slot = 0; phase ^= 1; }
   };
-  int ev = 0;                                  // record events so far
-  auto buf_of = [&]() { return ev % C::kBufs; };
-  auto buf_parity = [&]() { return static_cast<uint32_t>((ev / C::kBufs) & 1); };
-  auto rec_of = [&](int w, int half) { return rec + ((buf_of() * kMoeCW + w) * 2 + half) * C::kRec; };
+  int rbuf = 0;                                // record buffer of the current event
+  uint32_t rphase = 0;
+  auto next_event = [&]() {
+    if (++rbuf == a.bufs) { rbuf = 0; rphase ^= 1; }
+  };
+  auto rec_of = [&](int w, int half) { return rec + ((rbuf * kMoeCW + w) * 2 + half) * rec_floats; };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, s_abort, budget));
   };
@@ -462,10 +403,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
         const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
         const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
         if (k1.strips == 1) {
-          for (int j0 = ja; j0 < jb; j0 += BL)
+          for (int j0 = ja; j0 < jb; j0 += 2)
             for (int c = 0; c < k1.chunks; ++c) {
               const int p0 = c * k1.len, n = min(k1.len, k1.Q - p0);
-              for (int b = 0; b < 2 * min(BL, jb - j0); ++b) {
+              for (int b = 0; b < 2 * min(2, jb - j0); ++b) {
                 if (!open(n)) return;
                 copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j0 + (b >> 1)) * k1.Q + p0, n, gu_total);
                 close();
@@ -483,12 +424,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
         }
         u += jb - ja;
       }
-      for (int t0 = u2a; t0 < u2b; t0 += BL)
-        for (int x0 = 0; x0 < A; x0 += k2.strips) {
-          const int m = min(k2.strips, A - x0);
+      for (int t0 = u2a; t0 < u2b; t0 += 2)
+        for (int x0 = 0; x0 < V; x0 += k2.strips) {
+          const int m = min(k2.strips, V - x0);
           for (int c = 0; c < k2.chunks; ++c) {
             const int p0 = c * k2.len, n = min(k2.len, k2.Q - p0);
-            for (int b = 0; b < min(BL, u2b - t0); ++b) {
+            for (int b = 0; b < min(2, u2b - t0); ++b) {
               if (!open(m * n)) return;
               for (int i = 0; i < m; ++i)
                 copy(i * n, a.dn_q, a.dn_s, a.dn_z,
@@ -516,8 +457,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
     };
     auto done = [&]() {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&rempty[buf_of()]);
-      ++ev;
+      if (lane == 0) mbar_arrive(&rempty[rbuf]);
+      next_event();
     };
     bool ok = true;
     for (int u = u1a; ok && u < u1b;) {
@@ -525,7 +466,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
       const int first = l_first[x], cnt = l_first[x + 1] - first;
       const int per = k1.strips == 1 ? 1 : k1.strips / 2;               // units per event
       for (int j0 = ja; j0 < jb; j0 += per) {
-        ok = warp_wait(&rfull[buf_of()], buf_parity());
+        ok = warp_wait(&rfull[rbuf], rphase);
         if (!ok) break;
         const int nu = min(per, jb - j0);
         for (int q = lane; q < 16 * nu * cnt; q += 32) {
@@ -543,28 +484,18 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
       }
       u += jb - ja;
     }
-    // grid-wide barrier: every CTA's h is written (release) and visible (acquire)
+    // every CTA's h is written (release) and visible (acquire)
     __threadfence();
     __syncwarp();
-    if (ok && lane == 0) {
-      unsigned v;
-      asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(a.barrier) : "memory");
-      const uint64_t t0 = globaltimer_ns();
-      while (true) {
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a.barrier) : "memory");
-        if (v >= gridDim.x || *s_abort) break;
-        if (globaltimer_ns() - t0 > budget) {
-          *s_abort = 1;
-          atomicOr(&g_dev_status, kDevStatusTimeout);
-          break;
-        }
-      }
+    if (lane == 0) {
+      moe_await(moe_arrive(), s_abort, budget);
       if (*s_abort == 0) mbar_arrive(go);
     }
-    for (int t0 = u2a; ok && t0 < u2b; t0 += BL) {
-      ok = warp_wait(&rfull[buf_of()], buf_parity());
+    __syncwarp();   // the other lanes block here: polling ahead, they could keep lane 0 from its turn
+    for (int t0 = u2a; ok && t0 < u2b; t0 += 2) {
+      ok = warp_wait(&rfull[rbuf], rphase);
       if (!ok) break;
-      const int rows = 16 * min(BL, u2b - t0);
+      const int rows = 16 * min(2, u2b - t0);
       for (int q = lane; q < rows * a.T; q += 32) {
         const int row = q % rows, col = q / rows;
         if (!AWQ_CHECK(16 * t0 + row < a.K)) continue;
@@ -587,30 +518,22 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
     if (lane == 0) mbar_arrive(&empty[slot]);
     advance();
   };
-  auto rec_ready = [&]() { return warp_wait(&rempty[buf_of()], buf_parity() ^ 1); };
+  auto rec_ready = [&]() { return warp_wait(&rempty[rbuf], rphase ^ 1); };
   auto rec_done = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&rfull[buf_of()]);
-    ++ev;
+    if (lane == 0) mbar_arrive(&rfull[rbuf]);
+    next_event();
   };
-  // Fragments of an 8-token tile: `row` points at the lane's token (k 0), the group starts at k0.
-  auto load8 = [&](uint4 (&v)[2][2], const __half* row, int k0) {
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      v[kk][0] = ld_coherent_v4(row + k0 + kk * 64 + 16 * t);
-      v[kk][1] = ld_coherent_v4(row + k0 + kk * 64 + 16 * t + 8);
-    }
-  };
+  // The fragments of pair `pr` for a block's tokens, and their sums; `row` is the lane's token.
   auto load_frag = [&](MoeFrag& f, const __half* row, int pr, int G) {
-    load8(f.v[0], row, pr * 256);
-    if (2 * pr + 1 < G) {
-      load8(f.v[1], row, pr * 256 + 128);
-    } else {                                   // the padding group: its codes and scales are zero
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f.v[1][i >> 1][i & 1] = make_uint4(0, 0, 0, 0);
-    }
-  };
-  auto sum_frag = [&](MoeFrag& f) {
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          f.v[g][kk][i] = 2 * pr + g < G ? ld_coherent_v4(row + pr * 256 + g * 128 + kk * 64 + 16 * t + 8 * i)
+                                         : make_uint4(0, 0, 0, 0);   // the padding group
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       float d[4];
@@ -627,191 +550,123 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_experts_kernel(const M
       f.s[g][1] = d[1];
     }
   };
-  auto scale_of = [&](int item, int g) {
-    return *reinterpret_cast<const uint32_t*>(sb + kMoeOffS + item * kPairScaleBytes + g * 32 + r * 4);
-  };
-  auto zero_of = [&](int item, int g) { return static_cast<uint32_t>(sb[kMoeOffZ + item * kPairZeroBytes + g * 8 + r]); };
-  auto code_of = [&](int item, int g, int kk) {
-    return *reinterpret_cast<const uint4*>(sb + item * kPairCodeBytes + g * 1024 + kk * 512 + lane * 16);
-  };
-  auto pair8 = [&](float (&acc)[4], const MoeFrag& f, int item) {
-    const uint4 w[2][2] = {{code_of(item, 0, 0), code_of(item, 0, 1)}, {code_of(item, 1, 0), code_of(item, 1, 1)}};
-    const uint32_t sv[2] = {scale_of(item, 0), scale_of(item, 1)}, zz[2] = {zero_of(item, 0), zero_of(item, 1)};
+  // Adds the products of the stage's item with the fragments.
+  auto pair = [&](float (&acc)[4], const MoeFrag& f, int item) {
+    const uint8_t* cb = sb + item * kPairCodeBytes + lane * 16;
+    const uint8_t* sc = sb + kMoeOffS + item * kPairScaleBytes + r * 4;
+    const uint8_t* zb = sb + kMoeOffZ + item * kPairZeroBytes + r;
+    const uint4 w[2][2] = {{*reinterpret_cast<const uint4*>(cb), *reinterpret_cast<const uint4*>(cb + 512)},
+                           {*reinterpret_cast<const uint4*>(cb + 1024), *reinterpret_cast<const uint4*>(cb + 1536)}};
+    const uint32_t sv[2] = {*reinterpret_cast<const uint32_t*>(sc), *reinterpret_cast<const uint32_t*>(sc + 32)};
+    const uint32_t zz[2] = {zb[0], zb[8]};
     moe_pair(acc, w, f, sv, zz);
-  };
-  // More than 8 tokens: 16 at a time, group by group; the fragments do not stay in registers.
-  // `row_of(col)` is the lane's activation row for a column.
-  auto pair_many = [&](float (&acc)[MTT][4], int item, int pr, int G, int cnt, auto row_of) {
-    if constexpr (MTT > 1) {
-#pragma unroll
-      for (int b = 0; b < MTT / 2; ++b) {
-        if (16 * b >= cnt) break;
-        const __half* row[2] = {row_of(min(16 * b + r, cnt - 1)), row_of(min(16 * b + 8 + r, cnt - 1))};
-#pragma unroll 1
-        for (int g = 0; g < 2 && 2 * pr + g < G; ++g) {
-          uint4 v[2][2][2];                    // [64-k tile][token tile][half]
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            uint4 one[2][2];
-            load8(one, row[m], pr * 256 + g * 128);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i >> 1][m][i & 1] = one[i >> 1][i & 1];
-          }
-          float xs[2][2];
-          moe_sums<2>(xs, v);
-          moe_group<2>(reinterpret_cast<float(&)[2][4]>(acc[2 * b]), code_of(item, g, 0), code_of(item, g, 1), v, xs,
-                       scale_of(item, g), zero_of(item, g));
-        }
-      }
-    }
   };
   bool ok = true;
 
   // ---- phase 1
   {
-    float acc[BL][2][MTT][4] = {};
-    // this warp's sums of a tile become its record
-    auto record = [&](float (&v)[MTT][4], int half, int cnt) {
-      float* p = rec_of(warp, half);
-#pragma unroll
-      for (int m = 0; m < MTT; ++m)
-        if (8 * m < cnt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) p[(8 * m + 2 * t + (c & 1)) * 20 + r + 8 * (c >> 1)] = v[m][c];
-#pragma unroll
-      for (int m = 0; m < MTT; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[m][c] = 0.0f;
+    float acc[2][2][4] = {};
+    auto record = [&](float (&v)[4], int half) {
+      float* p = rec_of(warp, half) + 2 * t * 20 + r;
+      p[0] = v[0];
+      p[20] = v[1];
+      p[8] = v[2];
+      p[28] = v[3];
+      v[0] = v[1] = v[2] = v[3] = 0.0f;
     };
     const int pl = warp % k1.wide, sub = warp / k1.wide;
+    MoeFrag f;
     for (int u = u1a; ok && u < u1b;) {
       const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
       const int first = l_first[x], cnt = l_first[x + 1] - first;
-      auto row_of = [&](int col) { return a.x + static_cast<size_t>(l_token[first + col]) * a.K; };
-      const __half* row8 = row_of(min(r, cnt - 1));
-      // `many`: more than 8 tokens (separate code, so that its fragments and f do not share registers)
-      auto expert = [&](auto many) {
-        constexpr bool kMany = decltype(many)::value;
-        MoeFrag f;
-        if (k1.strips == 1) {
-          for (int j0 = ja; ok && j0 < jb; j0 += BL) {
-            const int nb = min(BL, jb - j0);
-            for (int c = 0; ok && c < k1.chunks; ++c) {
-              const int pr = c * k1.len + pl;
-              const bool live = pl < min(k1.len, k1.Q - c * k1.len);
-              if (!kMany && live && (k1.chunks > 1 || j0 == ja)) {   // one chunk: they last for the expert
-                load_frag(f, row8, pr, G1);
-                sum_frag(f);
-              }
+      // columns past the block's last token repeat it; they are never used
+      const __half* row = a.x + static_cast<size_t>(l_token[first + min(r, cnt - 1)]) * a.K;
+      if (k1.strips == 1) {
+        for (int j0 = ja; ok && j0 < jb; j0 += 2) {
+          const int nb = min(2, jb - j0);
+          for (int c = 0; ok && c < k1.chunks; ++c) {
+            const bool live = pl < min(k1.len, k1.Q - c * k1.len);
+            if (live && (k1.chunks > 1 || j0 == ja)) load_frag(f, row, c * k1.len + pl, G1);   // one chunk: once per block
 #pragma unroll
-              for (int b = 0; b < 2 * BL; ++b) {
-                if (b >= 2 * nb || !ok) break;
-                ok = take();
+            for (int b = 0; b < 4; ++b) {
+              if (b >= 2 * nb || !ok) break;
+              ok = take();
+              if (!ok) break;
+              if (live) pair(acc[b >> 1][b & 1], f, pl);
+              release();
+              if (c == k1.chunks - 1) {
+                if ((b & 1) == 0) ok = rec_ready();
                 if (!ok) break;
-                if (live) {
-                  if constexpr (kMany) pair_many(acc[b >> 1][b & 1], pl, pr, G1, cnt, row_of);
-                  else pair8(acc[b >> 1][b & 1][0], f, pl);
-                }
-                release();
-                if (c == k1.chunks - 1) {
-                  if ((b & 1) == 0) ok = rec_ready();
-                  if (!ok) break;
-                  record(acc[b >> 1][b & 1], b & 1, cnt);
-                  if (b & 1) rec_done();
-                }
+                record(acc[b >> 1][b & 1], b & 1);
+                if (b & 1) rec_done();
               }
             }
-          }
-        } else {
-          const int half = k1.strips / 2, i = sub % half;
-          if (!kMany && pl < k1.Q) {
-            load_frag(f, row8, pl, G1);
-            sum_frag(f);
-          }
-          for (int j0 = ja; ok && j0 < jb; j0 += half) {
-            ok = take();
-            if (!ok) break;
-            if (pl < k1.Q && j0 + i < jb) {
-              if constexpr (kMany) pair_many(acc[0][0], sub * k1.Q + pl, pl, G1, cnt, row_of);
-              else pair8(acc[0][0][0], f, sub * k1.Q + pl);
-            }
-            release();
-            ok = rec_ready();
-            if (!ok) break;
-            record(acc[0][0], 0, cnt);
-            rec_done();
           }
         }
-      };
-      if (MTT == 1 || cnt <= 8) expert(std::false_type{});
-      else expert(std::bool_constant<(MTT > 1)>{});
+      } else {
+        const int half = k1.strips / 2, i = sub % half;
+        if (pl < k1.Q) load_frag(f, row, pl, G1);
+        for (int j0 = ja; ok && j0 < jb; j0 += half) {
+          ok = take();
+          if (!ok) break;
+          if (pl < k1.Q && j0 + i < jb) pair(acc[0][0], f, sub * k1.Q + pl);
+          release();
+          ok = rec_ready();
+          if (!ok) break;
+          record(acc[0][0], 0);
+          rec_done();
+        }
+      }
       u += jb - ja;
     }
   }
 
   ok = ok && warp_wait(go, 0);
 
-  // ---- phase 2: an expert's sums are added to its tokens' places in the warp's record
+  // ---- phase 2: a block's sums are added to its tokens' places in the warp's record
   {
-    float acc[BL][MTT][4] = {};
+    float acc[2][4] = {};
     const int pl = warp % k2.wide, sub = warp / k2.wide;
-    for (int t0 = u2a; ok && t0 < u2b; t0 += BL) {
-      const int nb = min(BL, u2b - t0);
+    for (int t0 = u2a; ok && t0 < u2b; t0 += 2) {
+      const int nb = min(2, u2b - t0);
       ok = rec_ready();
       if (!ok) break;
-      for (int b = 0; b < nb; ++b)
-        for (int i = lane; i < a.T * 20; i += 32) rec_of(warp, b)[i] = 0.0f;
+      for (int i = lane; i < 2 * rec_floats; i += 32) rec_of(warp, 0)[i] = 0.0f;   // both halves
       __syncwarp();
-      for (int x0 = 0; ok && x0 < A; x0 += k2.strips) {
+      for (int x0 = 0; ok && x0 < V; x0 += k2.strips) {
         const int x = x0 + sub;
-        const bool mine = x < A;
+        const bool mine = x < V;
         const int first = mine ? l_first[x] : 0, cnt = mine ? l_first[x + 1] - first : 0;
-        auto row_of = [&](int col) { return a.h + static_cast<size_t>(first + col) * a.I; };
-        const __half* row8 = row_of(max(0, min(r, cnt - 1)));
-        auto expert = [&](auto many) {
-          constexpr bool kMany = decltype(many)::value;
-          for (int c = 0; ok && c < k2.chunks; ++c) {
-            const int n = min(k2.len, k2.Q - c * k2.len), pr = c * k2.len + pl;
-            const bool live = mine && pl < n;
-            MoeFrag f;
-            if (!kMany && live) {
-              load_frag(f, row8, pr, G2);
-              sum_frag(f);
-            }
+        const __half* row = a.h + static_cast<size_t>(first + max(0, min(r, cnt - 1))) * a.I;
+        for (int c = 0; ok && c < k2.chunks; ++c) {
+          const int n = min(k2.len, k2.Q - c * k2.len);
+          const bool live = mine && pl < n;
+          MoeFrag f;
+          if (live) load_frag(f, row, c * k2.len + pl, G2);
 #pragma unroll
-            for (int b = 0; b < BL; ++b) {
-              if (b >= nb || !ok) break;
-              ok = take();
-              if (!ok) break;
-              if (live) {
-                if constexpr (kMany) pair_many(acc[b], sub * n + pl, pr, G2, cnt, row_of);
-                else pair8(acc[b][0], f, sub * n + pl);
-              }
-              release();
-            }
+          for (int b = 0; b < 2; ++b) {
+            if (b >= nb || !ok) break;
+            ok = take();
+            if (!ok) break;
+            if (live) pair(acc[b], f, sub * n + pl);
+            release();
           }
-        };
-        if (MTT == 1 || cnt <= 8) expert(std::false_type{});
-        else expert(std::bool_constant<(MTT > 1)>{});
+        }
         if (!ok) break;
         if (mine && pl < k2.len) {
 #pragma unroll
-          for (int b = 0; b < BL; ++b) {
-            if (b >= nb) break;
-            float* p = rec_of(warp, b);
+          for (int c = 0; c < 2; ++c)
+            if (2 * t + c < cnt) {
+              float* p = rec_of(warp, 0) + l_token[first + 2 * t + c] * 20 + r;
 #pragma unroll
-            for (int m = 0; m < MTT; ++m)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int col = 8 * m + 2 * t + c;
-                if (col < cnt) {
-                  float* pt = p + l_token[first + col] * 20 + r;
-                  pt[0] += acc[b][m][c];
-                  pt[8] += acc[b][m][c + 2];
-                }
-                acc[b][m][c] = acc[b][m][c + 2] = 0.0f;
+              for (int b = 0; b < 2; ++b) {
+                if (b >= nb) break;
+                p[b * rec_floats] += acc[b][c];
+                p[b * rec_floats + 8] += acc[b][c + 2];
               }
-          }
+            }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
         }
       }
       if (ok) rec_done();
