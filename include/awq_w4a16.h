@@ -302,6 +302,9 @@ AWQ_API awq_status_t awq_search_alpha_noalloc(const uint16_t* x, const uint16_t*
  *   Like the decode kernel it starts reading wq before the preceding kernel of `stream` has
  *   completed (the prefetch rule of awq_w4a16_gemv, for which awq_quantize_channels lets no later
  *   kernel start early); xq, sx and sw are read after it.
+ * awq_w8a8_forward: awq_quantize_tokens, then awq_w8a8_linear, for a whole layer in one call. Its
+ *   workspace (device, 16-byte aligned, awq_w8a8_workspace_bytes: M*K rounded up to 256, + 4*M)
+ *   receives xq, then sx.
  * Require M >= 1, N >= 1 (both at most 2^31 - 128), 16 <= K <= AWQ_INT8_MAX_K, K % 16 == 0; x, s, W,
  * xq, wq and y 16-byte aligned. */
 #define AWQ_INT8_MAX_K 131056   /* (-128)^2 K < 2^31 */
@@ -311,6 +314,10 @@ AWQ_API awq_status_t awq_quantize_channels(const uint16_t* W, const float* fold_
                                            float* sw, awq_stream_t stream);
 AWQ_API awq_status_t awq_w8a8_linear(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, uint16_t* y,
                                      int M, int N, int K, awq_stream_t stream);
+AWQ_API size_t awq_w8a8_workspace_bytes(int M, int K);
+AWQ_API awq_status_t awq_w8a8_forward(const uint16_t* x, const float* s, const int8_t* wq, const float* sw, uint16_t* y,
+                                      int M, int N, int K, void* workspace, size_t workspace_bytes,
+                                      awq_stream_t stream);
 
 /* The residual update after a block and the RMS norm before the next one, with the activation
  * scaling of the next quantized linear layer (the 1/s of awq_scale_activations):

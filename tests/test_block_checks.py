@@ -45,6 +45,29 @@ def test_w8a8_refuses_before_any_device_call(lib):
     assert fn(V(A), V(A + 2), V(A), V(A), V(A), 1, 1, 16, None) == 3
 
 
+def test_w8a8_forward_refuses_before_any_device_call(lib):
+    need = lib.awq_w8a8_workspace_bytes(3, 48)
+    assert need == 256 + 12 and lib.awq_w8a8_workspace_bytes(1, 24) == 0 and lib.awq_w8a8_workspace_bytes(0, 16) == 0
+
+    def call(x=A, s=A, wq=A, sw=A, y=A, M=3, N=5, K=48, ws=A, n=need):
+        p = lambda v: None if v is None else V(v)  # noqa: E731
+        return lib.awq_w8a8_forward(p(x), p(s), p(wq), p(sw), p(y), M, N, K, p(ws), n, None)
+
+    for bad in (dict(x=None), dict(wq=None), dict(sw=None), dict(y=None), dict(ws=None), dict(n=need - 1), dict(M=0), dict(N=0),
+                dict(K=40), dict(K=131072, n=1 << 30)):
+        assert call(**bad) == 1, bad
+    for bad in (dict(x=MIS), dict(s=MIS), dict(wq=MIS), dict(y=MIS), dict(ws=MIS), dict(sw=A + 2)):
+        assert call(**bad) == 3, bad
+    with pytest.raises(ValueError, match="columns"):
+        P.validate_w8a8_forward(half(3, 32), torch.zeros((5, 16), dtype=torch.int8), torch.ones(5), None, None, require_cuda=False)
+    with pytest.raises(ValueError, match="K=32"):
+        P.validate_w8a8_forward(half(3, 32), torch.zeros((5, 32), dtype=torch.int8), torch.ones(5), torch.ones(16), None,
+                                require_cuda=False)
+    with pytest.raises(ValueError, match="shape"):
+        P.validate_w8a8_forward(half(3, 32), torch.zeros((5, 32), dtype=torch.int8), torch.ones(5), None, half(3, 4),
+                                require_cuda=False)
+
+
 def _norm(lib, y=A, r=A, g=A, per=1, pw=A, w=A, s=A, alpha=1.0, eps=1e-6, M=1, K=8, h=A, x=A):
     p = lambda v: None if v is None else V(v)  # noqa: E731
     return lib.awq_residual_norm(p(y), p(r), p(g), per, p(pw), p(w), p(s), alpha, eps, M, K, p(h), p(x), None)

@@ -18,7 +18,8 @@ Functions (same names as the C ABI):
 * ``awq_w4a16_linear_silu_mul(x, qweight, scales, zeros, I)`` -> h = SiLU(gate) * up
 * ``awq_search_alpha(x, W, alphas)`` -> (err[n] float64, best index): the AWQ scale search
 * ``awq_quantize_tokens(x, s)`` -> (xq int8, sx fp32); ``awq_quantize_channels(W, fold_scale)`` -> (wq, sw)
-* ``awq_w8a8_linear(xq, sx, wq, sw)`` -> y[M,N] fp16: the product in 8-bit integers; class ``AWQInt8Linear``
+* ``awq_w8a8_linear(xq, sx, wq, sw)`` -> y[M,N] fp16: the product in 8-bit integers;
+  ``awq_w8a8_forward(x, wq, sw, s)`` with the tokens' quantization; class ``AWQInt8Linear``
 * ``awq_residual_norm(y, residual, weight, ...)`` -> (h, x'): residual update, RMS norms, activation scaling
 * ``awq_moe_w4a16(x, router, gate_up, down, I, top_k)`` -> y[T,K]: a mixture-of-experts layer for a few
   tokens, experts in packed weights; class ``AWQMoE``
@@ -81,6 +82,8 @@ _SIGS = {
     "awq_quantize_tokens": ([_VP, _VP, _I, _I, _VP, _VP, _VP], _I),
     "awq_quantize_channels": ([_VP, _VP, _I, _I, _VP, _VP, _VP], _I),
     "awq_w8a8_linear": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP], _I),
+    "awq_w8a8_workspace_bytes": ([_I, _I], ctypes.c_size_t),
+    "awq_w8a8_forward": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, ctypes.c_size_t, _VP], _I),
     "awq_residual_norm": ([_VP, _VP, _VP, _I, _VP, _VP, _VP, ctypes.c_float, ctypes.c_float, _I, _I, _VP, _VP, _VP], _I),
     "awq_moe_workspace_bytes": ([_I, _I, _I, _I, _I], ctypes.c_size_t),
     "awq_moe_w4a16": ([_VP] * 9 + [_I] * 6 + [_VP, _VP, ctypes.c_size_t, _VP], _I),
@@ -142,22 +145,41 @@ def packed_nbytes(N: int, K: int) -> Tuple[int, int, int]:
 
 
 # ---------------------------------------------------------------------------- torch marshalling
+# The calls are a few microseconds of GPU work at their smallest, so the checks below are written to
+# cost little when they pass: one expression per tensor, the message worked out only on a failure.
+_torch_mod = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        _torch_mod = torch
+    return _torch_mod
+
+
+_raw_stream = None     # current stream handle of a device, without building a Stream object where torch allows it
 
 
 def _stream_ptr():
+    global _raw_stream
     torch = _torch()
-    return _VP(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is None:
+        torch.cuda.init()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
-def _ptr(t) -> _VP:
-    return _VP(t.data_ptr()) if t is not None else _VP(0)
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
 
 
 def _need(t, dtype, name, dims=None, require_cuda=True):
-    torch = _torch()
+    torch = _torch_mod or _torch()
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous() and (dims is None or t.dim() == dims) and
+            (not require_cuda or (t.is_cuda and t.get_device() == torch.cuda.current_device()))):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if require_cuda:
@@ -604,9 +626,46 @@ class AWQInt8Linear:
         wq, sw = awq_quantize_channels(W, s)
         return cls(wq, sw, s)
 
-    def __call__(self, x, y=None):
-        xq, sx = awq_quantize_tokens(x, self.s)
-        return awq_w8a8_linear(xq, sx, self.wq, self.sw, y)
+    def __call__(self, x, y=None, workspace=None):
+        return awq_w8a8_forward(x, self.wq, self.sw, self.s, y, workspace)
+
+
+def validate_w8a8_forward(x, wq, sw, s, y, require_cuda=True):
+    torch = _torch()
+    _need(x, torch.float16, "x", 2, require_cuda=require_cuda)
+    _need(wq, torch.int8, "wq", 2, require_cuda=require_cuda)
+    (M, K), (N, Kw) = x.shape, wq.shape
+    if M < 1 or N < 1:
+        raise ValueError("x and wq must have at least one row")
+    if Kw != K:
+        raise ValueError(f"wq must have K={K} columns, got {Kw}")
+    _check_int8_k(K)
+    _check_vec(sw, N, "sw", require_cuda)
+    if s is not None:
+        _check_vec(s, K, "s", require_cuda)
+    if y is not None:
+        _need(y, torch.float16, "y", 2, require_cuda=require_cuda)
+        if tuple(y.shape) != (M, N):
+            raise ValueError(f"y must have shape {(M, N)}, got {tuple(y.shape)}")
+
+
+def awq_w8a8_forward(x, wq, sw, s=None, y=None, workspace=None):
+    """A whole 8-bit linear layer: awq_quantize_tokens(x, s), then awq_w8a8_linear, in one call."""
+    validate_w8a8_forward(x, wq, sw, s, y)
+    (M, K), N = x.shape, wq.shape[0]
+    lib = load_library()
+    need = (M * K + 255) // 256 * 256 + 4 * M        # awq_w8a8_workspace_bytes(M, K)
+    if workspace is None:
+        workspace = wq.new_empty(need)
+    elif _need(workspace, wq.dtype, "workspace", 1) is None and workspace.numel() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    if y is None:
+        y = x.new_empty((M, N))
+    st = lib.awq_w8a8_forward(x.data_ptr(), _ptr(s), wq.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
+                              workspace.data_ptr(), need, _stream_ptr())
+    if st:
+        _check("awq_w8a8_forward", st)
+    return y
 
 
 # ---------------------------------------------------------------------------- residual update and norms
@@ -615,24 +674,27 @@ NORM_MAX_K = 32768
 
 def validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x, require_cuda=True):
     torch = _torch()
-    _need(y, torch.float16, "y", 2, require_cuda=require_cuda)
-    M, K = y.shape
+    f16 = torch.float16
+    _need(y, f16, "y", 2, require_cuda=require_cuda)
+    M, K = shape = y.shape
     if M < 1:
         raise ValueError("y must have at least one row")
     if K < 8 or K % 8 or K > NORM_MAX_K:
         raise ValueError(f"K must be a multiple of 8 in [8, {NORM_MAX_K}], got {K}")
     for t, name in ((residual, "residual"), (h, "h"), (x, "x")):
         if t is not None:
-            _need(t, torch.float16, name, 2, require_cuda=require_cuda)
-            if tuple(t.shape) != (M, K):
-                raise ValueError(f"{name} must have shape {(M, K)}, got {tuple(t.shape)}")
-    for t, name in ((weight, "weight"), (post_weight, "post_weight")):
-        if t is not None or name == "weight":
-            _need(t, torch.float16, name, 1, require_cuda=require_cuda)
-            if t.numel() != K:
-                raise ValueError(f"{name} must have K={K} elements, got {t.numel()}")
+            _need(t, f16, name, 2, require_cuda=require_cuda)
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _need(weight, f16, "weight", 1, require_cuda=require_cuda)
+    if weight.numel() != K:
+        raise ValueError(f"weight must have K={K} elements, got {weight.numel()}")
+    if post_weight is not None:
+        _need(post_weight, f16, "post_weight", 1, require_cuda=require_cuda)
+        if post_weight.numel() != K:
+            raise ValueError(f"post_weight must have K={K} elements, got {post_weight.numel()}")
     if gate is not None:
-        _need(gate, torch.float16, "gate", 2, require_cuda=require_cuda)
+        _need(gate, f16, "gate", 2, require_cuda=require_cuda)
         if gate.shape[1] != K or gate.shape[0] < 1 or M % gate.shape[0]:
             raise ValueError(f"gate must have K={K} columns and a number of rows that divides M={M}, "
                              f"got {tuple(gate.shape)}")
@@ -651,19 +713,24 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
     divisor of M: row m uses gate row m // (M // G). ``s`` is the next layer's stored scale.
     ``want_h=False`` leaves h unstored (the first result is None)."""
     torch = _torch()
-    _need(y, torch.float16, "y", 2)
-    M, K = y.shape
-    if out is None:
-        out = (torch.empty_like(y) if want_h else None, torch.empty_like(y))
-    h, x = out
+    h = x = None
+    if out is not None:
+        h, x = out
+        if x is None:
+            raise ValueError("x is always written")
     alpha, eps = float(alpha), float(eps)
-    if x is None:
-        raise ValueError("x is always written")
     validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
+    if out is None:
+        x = torch.empty_like(y)
+        if want_h:
+            h = torch.empty_like(y)
+    M, K = y.shape
     per = M // gate.shape[0] if gate is not None else 1
-    st = load_library().awq_residual_norm(_ptr(y), _ptr(residual), _ptr(gate), per, _ptr(post_weight), _ptr(weight),
-                                          _ptr(s), alpha, eps, M, K, _ptr(h), _ptr(x), _stream_ptr())
-    _check("awq_residual_norm", st)
+    st = load_library().awq_residual_norm(y.data_ptr(), _ptr(residual), _ptr(gate), per, _ptr(post_weight),
+                                          weight.data_ptr(), _ptr(s), alpha, eps, M, K, _ptr(h), x.data_ptr(),
+                                          _stream_ptr())
+    if st:
+        _check("awq_residual_norm", st)
     return h, x
 
 
@@ -712,25 +779,28 @@ def _validate_moe_tokens(x, y, E: int, K: int, require_cuda=True):
             raise ValueError(f"y must have shape {(T, K)}, got {tuple(y.shape)}")
 
 
-def _moe_call(x, router, gate_up, down, E, K, I, top_k, renormalize, h_scale, y, workspace):
+def _moe_call(x, router, gate_up, down, E, K, I, top_k, renormalize, h_scale, y, workspace, need=None):
     torch = _torch()
     lib = load_library()
     T = x.shape[0]
-    need = int(lib.awq_moe_workspace_bytes(T, E, K, I, top_k))
+    if need is None:
+        need = int(lib.awq_moe_workspace_bytes(T, E, K, I, top_k))
     if need == 0:
         raise ValueError("shape out of range for the mixture-of-experts layer")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = gate_up[2].new_empty(need)
     else:
         _need(workspace, torch.uint8, "workspace", 1)
         if workspace.numel() < need:
             raise ValueError(f"workspace must hold {need} bytes")
     if y is None:
         y = torch.empty_like(x)
-    st = lib.awq_moe_w4a16(_ptr(x), _ptr(router), *[_ptr(t) for t in gate_up], *[_ptr(t) for t in down], _ptr(h_scale),
-                           T, E, K, I, top_k, int(bool(renormalize)), _ptr(y), _ptr(workspace), workspace.numel(),
-                           _stream_ptr())
-    _check("awq_moe_w4a16", st)
+    st = lib.awq_moe_w4a16(x.data_ptr(), router.data_ptr(), gate_up[0].data_ptr(), gate_up[1].data_ptr(),
+                           gate_up[2].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), down[2].data_ptr(),
+                           _ptr(h_scale), T, E, K, I, top_k, 1 if renormalize else 0, y.data_ptr(),
+                           workspace.data_ptr(), need, _stream_ptr())
+    if st:
+        _check("awq_moe_w4a16", st)
     return y
 
 
@@ -762,6 +832,8 @@ class AWQMoE:
         if s is not None:
             _check_vec(s, self.K, "s")
         self.router, self.gate_up, self.down, self.h_scale, self.s = router, tuple(gate_up), tuple(down), h_scale, s
+        self._need = [int(load_library().awq_moe_workspace_bytes(t, self.E, self.K, self.I, self.top_k))
+                      for t in range(MOE_MAX_TOKENS + 1)]    # workspace bytes by the number of tokens
 
     @classmethod
     def from_float(cls, router, W_gate_up, W_down, top_k: int, x_calib=None, alpha: float = 0.5, renormalize: bool = True,
@@ -789,4 +861,4 @@ class AWQMoE:
         if self.s is not None and not scaled:
             x = awq_scale_activations(x, self.s)
         return _moe_call(x, self.router, self.gate_up, self.down, self.E, self.K, self.I, self.top_k, self.renormalize,
-                         self.h_scale, y, workspace)
+                         self.h_scale, y, workspace, self._need[x.shape[0]])

@@ -135,28 +135,24 @@ __global__ void __launch_bounds__(1024) awq_quantize_rows_kernel(const __half* _
 // ---------------------------------------------------------------------------- int8 product
 // The weights are the MMA's A operand (rows = output channels), the tokens its B operand (columns),
 // so one kernel serves one token (BT = 16 columns) and a long prompt (BT = 256). Per CTA:
-//   warp 0 (one lane): producer — per 128-byte k block one TMA box of `rows` weight rows and one of
+//   warp 0 (one lane): producer — per 128-byte k block one TMA box of the tile's weight rows and one of
 //       BT token rows (128-byte swizzle, zero fill past M, N and K) into a ring; the first ring
 //       pass of weights is requested before the wait on the stream's predecessor;
 //   warp 1 (one lane): tcgen05.mma kind::i8, 128 x BT x 32 per instruction, int32 in tensor memory;
-//   warps 2..5: epilogue — tcgen05.ld, scales in fp32, coalesced fp16 stores.
-// A tile has `rows` <= 128 MT weight rows (a multiple of 8), chosen on the host so that the row
-// blocks fill the SMs in one wave when the layer is bound by its weight bytes. The MMA always reads
-// 128 MT rows of shared memory; what lies behind the tile's rows only reaches accumulator rows that
-// are never stored. ks > 1: the CTAs of a cluster split a tile's k blocks, and each adds the int32
-// partial sums (exact in any order) of its share of the token columns from distributed shared memory.
+//   warps 2..: epilogue — tcgen05.ld, scales in fp32, fp16 stores, the channels of a warp side by side.
+// A tile has 128 MT weight rows. ks > 1: the CTAs of a cluster split a tile's k blocks, and each adds
+// the int32 partial sums (exact in any order) of its share of the token columns from distributed
+// shared memory.
 struct Int8Args {
   const float* sx;
   const float* sw;
   __half* y;
   int M, N, K;
-  int rows;         // weight rows per tile
-  int row_blocks, tok_tiles;
+  int row_blocks, tok_tiles;   // tiles along N and M
   int ks;           // CTAs per tile (cluster size); > 1: one tile per cluster
   int stages, kpb;  // ring stages; 128-byte k blocks per stage
 };
 
-constexpr int kI8Threads = 192;
 constexpr int kI8MaxStages = 16;
 constexpr int kI8Bars = 2 * kI8MaxStages + 5;
 constexpr int kI8SmemMax = 232448;
@@ -164,10 +160,15 @@ constexpr int kI8Fixed = kI8Bars * 8 + 16 + 1024;    // barriers, tensor-memory 
 
 template <int BT, int MT>
 struct Int8Cfg {
+  // epilogue warps: one per tensor-memory lane quarter, two where a tile has many columns
+  static constexpr int kEpi = BT >= 128 ? 8 : 4;
+  static constexpr int kThreads = 32 * (2 + kEpi);
+  static constexpr int kCols = BT / (kEpi / 4);              // token columns of an epilogue warp
+  static constexpr int kSxBytes = kEpi * kCols * 4;          // their sx, a copy per warp
   static constexpr int kAcc = MT * BT;                       // accumulator columns
   static constexpr int kNAcc = 2 * kAcc <= 512 ? 2 : 1;      // two let an epilogue overlap the next tile
-  static constexpr int kCols = kNAcc * kAcc <= 32 ? 32 : kNAcc * kAcc;
-  static_assert((kCols & (kCols - 1)) == 0 && kCols <= 512, "tensor memory");
+  static constexpr int kTmem = kNAcc * kAcc <= 32 ? 32 : kNAcc * kAcc;
+  static_assert((kTmem & (kTmem - 1)) == 0 && kTmem <= 512, "tensor memory");
   static constexpr int kChunk = BT < 32 ? 16 : 32;           // accumulator columns per tcgen05.ld
 };
 
@@ -199,24 +200,31 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld_32x32b_x16(taddr, v); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
 
-__device__ __forceinline__ int ld_cluster_s32(uint32_t cluster_addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
   return v;
+}
+__device__ __forceinline__ __half i8_out(int sum, float sx, float sw) {
+  return __float2half_rn(static_cast<float>(sum) * (sx * sw));
 }
 
 template <int BT, int MT>
-__global__ void __launch_bounds__(kI8Threads, 1)
+__global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
     awq_w8a8_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
                     const Int8Args a) {
   using C = Int8Cfg<BT, MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = a.stages, kpb = a.kpb;
-  const int a_bytes = a.rows * 128, b_bytes = BT * 128;              // one k block
+  constexpr int kRows = 128 * MT, a_bytes = kRows * 128, b_bytes = BT * 128;   // one k block
   const int stage_bytes = kpb * (a_bytes + b_bytes);
-  const int ring_bytes = S * stage_bytes + MT * 16384 - a_bytes;     // + what the last MMA reads past its rows
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes);
+  const int ring_bytes = S * stage_bytes;
+  float* s_sx = reinterpret_cast<float*>(smem + ring_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes + C::kSxBytes);
   uint64_t* empty = full + kI8MaxStages;
   uint64_t* accfull = empty + kI8MaxStages;
   uint64_t* accempty = accfull + 2;
@@ -250,7 +258,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
-      mbar_init(&accempty[b], 4);
+      mbar_init(&accempty[b], C::kEpi);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -261,7 +269,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     tma_prefetch_desc(&tmap_x);
   }
   if (warp == 1) {
-    tmem_alloc(s_tmem, C::kCols);
+    tmem_alloc(s_tmem, C::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -277,7 +285,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       auto issue_w = [&](int slot, int rb, int kb, int n) {
         uint8_t* sb = smem + slot * stage_bytes;
         mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(n * (a_bytes + b_bytes)));
-        for (int j = 0; j < n; ++j) tma_load_2d(sb + j * a_bytes, &tmap_w, (kb + j) * 128, rb * a.rows, &full[slot]);
+        for (int j = 0; j < n; ++j) tma_load_2d(sb + j * a_bytes, &tmap_w, (kb + j) * 128, rb * kRows, &full[slot]);
       };
       auto issue_x = [&](int slot, int tt, int kb, int n) {
         uint8_t* sb = smem + slot * stage_bytes + kpb * a_bytes;
@@ -354,39 +362,71 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     // ------------------------------------------------------------ epilogue
     pdl_wait();
     const int e = warp & 3;                    // tensor-memory lane quarter of this warp
+    const int cw = (warp - 2) >> 2;            // its part of the token columns
     constexpr int CH = C::kChunk;
+    float* my_sx = s_sx + (warp - 2) * C::kCols;
+    // channels in pairs: with an even N, the lanes of a pair trade values of two tokens, so that each
+    // stores both channels of one token in four bytes
+    const bool paired = (a.N & 1) == 0;
     bool ok = true;
     int it = 0;
     for (int t = tile0; ok && t < ntiles; t += step, ++it) {
       int rb, tt;
       tile_at(t, rb, tt);
+      const int tok0 = tt * BT + cw * C::kCols;
+      if (ks == 1) {
+        __syncwarp();
+        for (int i = lane; i < C::kCols; i += 32) my_sx[i] = tok0 + i < a.M ? __ldg(a.sx + tok0 + i) : 0.0f;
+        __syncwarp();
+      }
       const int b = it % C::kNAcc;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&accfull[b], (it / C::kNAcc) & 1, s_abort, budget))) { ok = false; break; }
       tc_fence_after();
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int lr = m * 128 + 32 * e + lane;              // row within the tile
-        const long long n = static_cast<long long>(rb) * a.rows + lr;
-        const bool n_ok = lr < a.rows && n < a.N;
+        const long long n = static_cast<long long>(rb) * kRows + lr;
+        const bool n_ok = n < a.N;
         const float sw = ks == 1 && n_ok ? __ldg(a.sw + n) : 0.0f;
 #pragma unroll 1
-        for (int c0 = 0; c0 < BT; c0 += CH) {
+        for (int c0 = 0; c0 < C::kCols; c0 += CH) {
+          if (ks == 1 && tok0 + c0 >= a.M) break;
           uint32_t v[CH];
           tmem_ld_cols(tmem_base + (static_cast<uint32_t>(32 * e) << 16) +
-                           static_cast<uint32_t>(b * C::kAcc + m * BT + c0), v);
+                           static_cast<uint32_t>(b * C::kAcc + m * BT + cw * C::kCols + c0), v);
           tc_wait_ld();
           if (ks > 1) {                                      // the ring is idle: partial sums take its place
-            int* part = reinterpret_cast<int*>(smem) + (m * BT + c0) * 128 + 32 * e + lane;
+            int* part = reinterpret_cast<int*>(smem) + (m * BT + cw * C::kCols + c0) * 128 + 32 * e + lane;
 #pragma unroll
             for (int j = 0; j < CH; ++j) part[j * 128] = static_cast<int>(v[j]);
+            continue;
+          }
+          __half o[CH];
+#pragma unroll
+          for (int j = 0; j < CH; j += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(my_sx + c0 + j);
+            o[j] = i8_out(static_cast<int>(v[j]), s4.x, sw);
+            o[j + 1] = i8_out(static_cast<int>(v[j + 1]), s4.y, sw);
+            o[j + 2] = i8_out(static_cast<int>(v[j + 2]), s4.z, sw);
+            o[j + 3] = i8_out(static_cast<int>(v[j + 3]), s4.w, sw);
+          }
+          if (paired) {
+            const int odd = lane & 1;
+            __half* p = a.y + static_cast<size_t>(tok0 + c0 + odd) * a.N + (n - odd);
+            const int left = a.M - (tok0 + c0 + odd);
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) {
+              const uint32_t own = (static_cast<uint32_t>(__half_as_ushort(o[j + 1])) << 16) | __half_as_ushort(o[j]);
+              const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+              // even lanes: token j of both channels; odd lanes: token j + 1
+              const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+              if (n_ok && j < left) *reinterpret_cast<uint32_t*>(p) = w;
+              p += 2 * static_cast<size_t>(a.N);
+            }
           } else if (n_ok) {
 #pragma unroll
-            for (int j = 0; j < CH; ++j) {
-              const int tok = tt * BT + c0 + j;
-              if (tok < a.M)
-                a.y[static_cast<size_t>(tok) * a.N + n] =
-                    __float2half_rn(static_cast<float>(static_cast<int>(v[j])) * (__ldg(a.sx + tok) * sw));
-            }
+            for (int j = 0; j < CH; ++j)
+              if (tok0 + c0 + j < a.M) a.y[static_cast<size_t>(tok0 + c0 + j) * a.N + n] = o[j];
           }
         }
       }
@@ -400,7 +440,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::kCols);
+    tmem_dealloc(tmem_base, C::kTmem);
   }
   if (ks > 1) {
     cluster_arrive();
@@ -410,20 +450,34 @@ __global__ void __launch_bounds__(kI8Threads, 1)
       tile_at(tile0, rb, tt);
       const int c_lo = rank * BT / ks, c_hi = min((rank + 1) * BT / ks, a.M - tt * BT);
       const uint32_t base = smem_u32(smem);
-      for (int i = threadIdx.x; i < (c_hi - c_lo) * a.rows; i += kI8Threads) {
-        const int c = c_lo + i / a.rows, lr = i % a.rows;
-        const long long n = static_cast<long long>(rb) * a.rows + lr;
-        if (n >= a.N) continue;
-        const uint32_t off = (((lr >> 7) * BT + c) * 128 + (lr & 127)) * 4;
-        int sum = 0;
-        for (int r = 0; r < ks; ++r) {
+      constexpr int quads = kRows / 4;
+      for (int i = threadIdx.x; i < (c_hi - c_lo) * quads; i += C::kThreads) {
+        const int c = c_lo + i / quads, lr = i % quads * 4;   // four rows of one column
+        const long long n = static_cast<long long>(rb) * kRows + lr;
+        const uint32_t off = base + (((lr >> 7) * BT + c) * 128 + (lr & 127)) * 4;
+        int4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          if (r >= ks) break;
           uint32_t addr;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + off), "r"(r));
-          sum += ld_cluster_s32(addr);
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(off), "r"(r));
+          v[r] = ld_cluster_v4(addr);
+        }
+        int sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          if (r >= ks) break;
+          sum[0] += v[r].x;
+          sum[1] += v[r].y;
+          sum[2] += v[r].z;
+          sum[3] += v[r].w;
         }
         const int tok = tt * BT + c;
-        a.y[static_cast<size_t>(tok) * a.N + n] =
-            __float2half_rn(static_cast<float>(sum) * (__ldg(a.sx + tok) * __ldg(a.sw + n)));
+        const float sx = __ldg(a.sx + tok);
+        __half* p = a.y + static_cast<size_t>(tok) * a.N + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j < a.N) p[j] = i8_out(sum[j], sx, __ldg(a.sw + n + j));
       }
     }
     cluster_arrive();

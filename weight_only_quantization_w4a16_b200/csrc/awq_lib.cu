@@ -582,39 +582,49 @@ awq_status_t make_i8_map(CUtensorMap* map, const void* q, int rows, int K, int b
   return r == CUDA_SUCCESS ? AWQ_OK : AWQ_ERR_CUDA;
 }
 
-// Token tile, weight rows per tile and K split of the int8 kernel. A CTA's time is modelled in
-// cycles per 128-byte k block: the larger of its share of the HBM stream (rows * 128 bytes at 23
-// bytes per cycle and SM) and of its four MMAs per 128 rows (at least 47 cycles each to issue, BT / 2
-// at full rate), plus a fixed cost per tile and per cluster exchange. With M <= 64 the rows per tile
-// are chosen so that all SMs share the weight rows evenly; above, tiles are 128 rows.
+// Token tile, weight rows per tile and K split of the int8 kernel.
+// M <= 64 is bound by the weight bytes, and what counts is how many copies are under way: two CTAs fit
+// an SM (half of its shared memory each), and the form with the most CTAs, up to two per SM, wins;
+// among equals the larger K split with the taller tiles (measured at M = 1: 4096 x 4096 7.3 us with 256
+// CTAs against 9.5 with 128 of 32 rows each; 12288 x 4096 12.4 against 14.6; 28672 x 4096 22.6
+// against 24.1; 4096 x 14336 13.3 against 15.4).
+// Above, a tile takes about `step` cycles per 128-byte k block: L2 delivers some 64 bytes per cycle
+// to an SM, so 256 token columns cost little more than 128 (750, 690 and 560 cycles for 256, 128 and 64,
+// measured). A K split saves rounds of a small grid but pays for the exchange (1500 + 30 per column:
+// 512 x 4096 x 14336 32.5 us with it, 46.9 without), and never pays beyond one round.
 struct Int8Plan {
   int bt, mt, rows, ks;
 };
 Int8Plan int8_plan(int M, int N, int K, int num_sms) {
   const int KB = ceil_div(K, 128);
+  if (M <= 64) {
+    Int8Plan best = {M <= 16 ? 16 : M <= 32 ? 32 : 64, 2, 256, 1};
+    long long most = 0;
+    for (int mt = 1; mt <= 2; ++mt)
+      for (int ks = 1; ks <= 8 && ks <= KB; ks *= 2) {
+        const long long ctas = static_cast<long long>(ceil_div(N, 128 * mt)) * ks;
+        if (ctas <= 2 * num_sms && ctas >= most) {
+          most = ctas;
+          best.mt = mt;
+          best.rows = 128 * mt;
+          best.ks = ks;
+        }
+      }
+    return best;
+  }
   Int8Plan best = {256, 1, 128, 1};
   double best_cost = 1e300;
-  auto consider = [&](int bt, int rows, int ks) {
-    const int mt = rows > 128 ? 2 : 1;
-    const long long tiles = static_cast<long long>(ceil_div(N, rows)) * ceil_div(M, bt);
-    const long long slots = std::max(1, num_sms / ks);
-    const double mma = 4.0 * mt * std::max(47.0, bt / 2.0);
-    const double stream = rows * 128.0 / 23.0;
-    const double cost = static_cast<double>((tiles + slots - 1) / slots) *
-                        (ceil_div(KB, ks) * std::max(mma, stream) + 600.0 + 2.0 * bt + (ks > 1 ? 1500.0 : 0.0));
-    if (cost < best_cost) { best_cost = cost; best = {bt, mt, rows, ks}; }
-  };
-  for (int ks = 1; ks <= 8 && ks <= KB && ks <= num_sms; ks *= 2) {
-    if (M <= 64) {
-      const long long slots = num_sms / ks;
-      const long long rounds = (N + slots * 256 - 1) / (slots * 256);
-      const int rows = std::min(256, round_up(static_cast<int>((N + slots * rounds - 1) / (slots * rounds)), 8));
-      if (ks > 1 && rounds > 1) continue;
-      consider(M <= 16 ? 16 : M <= 32 ? 32 : 64, rows, ks);
-    } else {
-      consider(64, 128, ks);
-      consider(128, 128, ks);
-      if (M > 128) consider(256, 128, ks);
+  for (int bt = 256; bt >= 64; bt /= 2) {
+    const double step = bt == 256 ? 750.0 : bt == 128 ? 690.0 : 560.0;
+    const long long tiles = static_cast<long long>(ceil_div(N, 128)) * ceil_div(M, bt);
+    const long long slots = bt == 64 ? 2 * num_sms : num_sms;
+    for (int ks = 1; ks <= 4 && ks <= KB; ks *= 2) {
+      const long long ctas = tiles * ks;
+      if (ks > 1 && ctas > slots) break;
+      const double shared = std::min(ctas, slots) > num_sms ? 1.33 : 1.0;   // two CTAs on an SM
+      const double cost = static_cast<double>((ctas + slots - 1) / slots) * (ceil_div(KB, ks) * step * shared + 2000.0) +
+                          (ks > 1 ? 1500.0 + 30.0 * bt : 0.0);
+      if (cost < best_cost) { best_cost = cost; best = {bt, 1, 128, ks}; }
     }
   }
   return best;
@@ -627,20 +637,23 @@ awq_status_t launch_w8a8_cfg(const int8_t* xq, const float* sx, const int8_t* wq
   static std::atomic<uint64_t> smem_done{0};
   awq_status_t st = ensure_smem(kernel, kI8SmemMax, dev, smem_done);
   if (st != AWQ_OK) return st;
-  Int8Args a = {sx, sw, y, M, N, K, p.rows, ceil_div(N, p.rows), ceil_div(M, BT), p.ks, 0, 0};
+  Int8Args a = {sx, sw, y, M, N, K, ceil_div(N, p.rows), ceil_div(M, BT), p.ks, 0, 0};
   const int KB = ceil_div(K, 128), steps = ceil_div(KB, p.ks);
   const int block = (p.rows + BT) * 128;
   a.kpb = std::max(1, std::min(std::min(4, steps), 24576 / block));
-  const int pad = MT * 16384 - p.rows * 128;
-  a.stages = std::min(kI8MaxStages, (kI8SmemMax - kI8Fixed - pad) / (a.kpb * block));
+  // M <= 64: at most half of an SM's shared memory, so that the next call's CTAs can already be
+  // resident and read their first weights while this one's end (a stream of 96 KB per SM is enough)
+  constexpr int pad = Int8Cfg<BT, MT>::kSxBytes;
+  const int cap = BT <= 64 ? kI8SmemMax / 2 : kI8SmemMax;
+  a.stages = std::max(2, std::min(kI8MaxStages, (cap - kI8Fixed - pad) / (a.kpb * block)));
   const long long tiles = static_cast<long long>(a.row_blocks) * a.tok_tiles;
   if (tiles * p.ks > (1ll << 30)) return AWQ_ERR_INVALID_ARG;
   const size_t smem = static_cast<size_t>(a.stages) * a.kpb * block + pad + kI8Fixed;
   CUtensorMap wmap, xmap;
   if ((st = make_i8_map(&wmap, wq, N, K, p.rows)) != AWQ_OK) return st;
   if ((st = make_i8_map(&xmap, xq, M, K, BT)) != AWQ_OK) return st;
-  const long long grid = p.ks > 1 ? tiles * p.ks : std::min<long long>(tiles, num_sms);
-  return launch_ex(kernel, dim3(static_cast<unsigned>(grid), 1, 1), dim3(kI8Threads, 1, 1),
+  const long long grid = p.ks > 1 ? tiles * p.ks : std::min<long long>(tiles, (BT <= 64 ? 2ll : 1ll) * num_sms);
+  return launch_ex(kernel, dim3(static_cast<unsigned>(grid), 1, 1), dim3(Int8Cfg<BT, MT>::kThreads, 1, 1),
                    p.ks > 1 ? dim3(p.ks, 1, 1) : dim3(0, 0, 0), smem, stream, wmap, xmap, a);
 }
 
@@ -686,6 +699,17 @@ awq_status_t check_linear_args(const void* x, const void* qw, const void* sc, co
 // Packed sizes of layout v2: per (16-row tile, group pair) 2048 + 64 + 16 bytes.
 inline size_t tile_pairs(int N, int K) {
   return static_cast<size_t>(ceil_div(N, kTileRows)) * static_cast<size_t>(ceil_div(K / kGroup, 2));
+}
+
+awq_status_t check_w8a8_args(const void* xq, const void* sx, const void* wq, const void* sw, const void* y, int M, int N,
+                             int K) {
+  if (!xq || !sx || !wq || !sw || !y) return AWQ_ERR_INVALID_ARG;
+  if (M < 1 || N < 1 || N > kMaxRows || K < 16 || K % 16 != 0 || K > AWQ_INT8_MAX_K) return AWQ_ERR_INVALID_ARG;
+  if (M > kMaxRows) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(sx) & 3u) ||
+      (reinterpret_cast<uintptr_t>(sw) & 3u))
+    return AWQ_ERR_MISALIGNED;
+  return AWQ_OK;
 }
 
 // Workspace of the scale search, each piece 256-byte aligned: y_ref fp32 [M,N], y fp16 [M,N], s fp32 [K],
@@ -1058,17 +1082,31 @@ awq_status_t awq_quantize_channels(const uint16_t* W, const float* fold_scale, i
 
 awq_status_t awq_w8a8_linear(const int8_t* xq, const float* sx, const int8_t* wq, const float* sw, uint16_t* y, int M,
                              int N, int K, awq_stream_t stream) {
-  if (!xq || !sx || !wq || !sw || !y) return AWQ_ERR_INVALID_ARG;
-  if (M < 1 || N < 1 || N > kMaxRows || K < 16 || K % 16 != 0 || K > AWQ_INT8_MAX_K) return AWQ_ERR_INVALID_ARG;
-  if (M > kMaxRows) return AWQ_ERR_INVALID_ARG;
-  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(sx) & 3u) ||
-      (reinterpret_cast<uintptr_t>(sw) & 3u))
-    return AWQ_ERR_MISALIGNED;
-  int dev, sms;
-  const awq_status_t st = current_device(&dev, &sms);
+  awq_status_t st = check_w8a8_args(xq, sx, wq, sw, y, M, N, K);
   if (st != AWQ_OK) return st;
+  int dev, sms;
+  if ((st = current_device(&dev, &sms)) != AWQ_OK) return st;
   return launch_w8a8(xq, sx, wq, sw, reinterpret_cast<__half*>(y), M, N, K, dev, sms,
                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t awq_w8a8_workspace_bytes(int M, int K) {
+  if (M < 1 || M > kMaxRows || K < 16 || K % 16 != 0 || K > AWQ_INT8_MAX_K) return 0;
+  return align256(static_cast<size_t>(M) * K) + static_cast<size_t>(M) * 4;
+}
+
+awq_status_t awq_w8a8_forward(const uint16_t* x, const float* s, const int8_t* wq, const float* sw, uint16_t* y, int M,
+                              int N, int K, void* workspace, size_t workspace_bytes, awq_stream_t stream) {
+  const size_t need = awq_w8a8_workspace_bytes(M, K);
+  if (!workspace || need == 0 || workspace_bytes < need) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return AWQ_ERR_MISALIGNED;
+  int8_t* xq = static_cast<int8_t*>(workspace);
+  float* sx = reinterpret_cast<float*>(xq + align256(static_cast<size_t>(M) * K));
+  // both calls' arguments are checked before the first launch
+  awq_status_t st = check_w8a8_args(xq, sx, wq, sw, y, M, N, K);
+  if (st != AWQ_OK) return st;
+  if ((st = awq_quantize_tokens(x, s, M, K, xq, sx, stream)) != AWQ_OK) return st;
+  return awq_w8a8_linear(xq, sx, wq, sw, y, M, N, K, stream);
 }
 
 awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, const uint16_t* gate, int rows_per_gate,
