@@ -1139,8 +1139,10 @@ awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, cons
     return launch_ex(kernel, dim3(static_cast<unsigned>(M), 1, 1), dim3(round_up(ceil_div(chunks, vpt), 32), 1, 1),
                      dim3(0, 0, 0), 0, reinterpret_cast<cudaStream_t>(stream), a);
   };
-  if (chunks <= 512) return run(awq_residual_norm_kernel<1>, 1);
-  if (chunks <= 2048) return run(awq_residual_norm_kernel<2>, 2);
+  const bool many = M >= 4 * sms;
+  if (chunks <= (many ? 256 : 1024)) return run(awq_residual_norm_kernel<1>, 1);
+  const bool deep = a.post_w != nullptr && M >= 16 * sms && chunks >= 512;
+  if (!deep && chunks <= 2 * norm_max_threads(2)) return run(awq_residual_norm_kernel<2>, 2);
   return run(awq_residual_norm_kernel<4>, 4);
 }
 

@@ -9,7 +9,12 @@
 // scaled down by s), so x' goes straight into a quantized linear call.
 //
 // Bound by HBM: 8 bytes per value (10 with a gate per token). One CTA per row; the row stays in
-// registers between the two means, so every input is read once.
+// registers between the two means, so every input is read once. Few rows (a decoding batch) are bound
+// by latency and take as many threads as they have 8-value chunks; many rows two chunks per thread,
+// four where the norm after the block adds a second reduction and many rows hide it.
+// Measured: 8192 x 8192 83 us (0.98 of the copy rate; 95 with the IEEE division by s), 90 us with the
+// norm after the block (98 with two chunks per thread); 1023 x 11016 with a gate per token 20 us (0.84);
+// 1 x 4096 2.1 us.
 #pragma once
 
 #include "awq_common.cuh"
@@ -61,8 +66,12 @@ __device__ __forceinline__ float block_sum(float v, float* s_part) {
   return v;
 }
 
+// Threads that a row takes with VPT 8-value chunks per thread: at most 768 with two chunks, so that two
+// CTAs fit an SM's registers.
+constexpr int norm_max_threads(int vpt) { return vpt == 2 ? 768 : 1024; }
+
 template <int VPT>
-__global__ void __launch_bounds__(1024) awq_residual_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kernel(const NormArgs a) {
   pdl_enter_early();
   __shared__ float s_part[2][32];
   const size_t row = blockIdx.x;
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(1024) awq_residual_norm_kernel(const NormArgs 
       const float4 s1 = __ldg(reinterpret_cast<const float4*>(a.s + c * 8 + 4));
       const float sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = __fdiv_rn(w[j], sc[j]);
+      for (int j = 0; j < 8; ++j) w[j] = __fdividef(w[j], sc[j]);   // 2 units of 2^-24: far below the fp16 step
     }
     *reinterpret_cast<uint4*>(a.x + base + c * 8) = pack8(w);
   }
