@@ -14,12 +14,40 @@
 namespace awq {
 
 // ---------------------------------------------------------------------------- row quantizer
-// One CTA per row. A row that fits (K <= 8 VPT threads) stays in registers between the maximum
-// and the codes, so it is read once: 3 bytes of traffic per value. The maximum is taken on the
-// fp16 magnitude bits as integers: exact, and a NaN compares above every number, so it reaches
-// the row's step instead of being dropped.
+// One CTA per row. A row that fits (K <= 8 VPT threads) stays in registers between the maximum and the
+// codes, so it is read once: 3 bytes of traffic per value. The maximum is taken on the fp16 magnitude
+// bits as integers: exact, and a NaN compares above every number, so it reaches the row's step instead
+// of being dropped. The codes' IEEE quotients come from a reciprocal per row and two corrections on pairs
+// of values (6 instructions a pair).
 enum RowScale { kRowPlain = 0, kRowDivide = 1, kRowMultiply = 2 };
 
+__device__ __forceinline__ float2 fma_rn2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul_rn2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+// RN(v / d) for two values, with minus_d = -d and r = RN(1 / d). The product v r is off by less than 1.5
+// units in the last place and the first residual correction leaves an error just above half a unit; from
+// such a quotient and a correctly rounded reciprocal the second gives RN(v / d) (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990). Exact as long as no step
+// under- or overflows: v is 0 or a finite fp16 value, d a row's step.
+__device__ __forceinline__ float2 div_rn2(float2 v, float2 minus_d, float2 r) {
+  float2 q = mul_rn2(v, r);
+  q = fma_rn2(fma_rn2(minus_d, q, v), r, q);
+  return fma_rn2(fma_rn2(minus_d, q, v), r, q);
+}
+
+// fp16(v / s) or fp16(v * s) of eight values.
 template <int MODE>
 __device__ __forceinline__ uint4 row_scaled(uint4 v, const float* __restrict__ s, int k) {
   if (MODE == kRowPlain) return v;
@@ -45,26 +73,17 @@ __device__ __forceinline__ uint32_t max_abs_bits(uint32_t m, const uint4& v) {
   return __vmaxu2(m, v.w & 0x7FFF7FFFu);
 }
 
-// rint(RN(v / step)) for eight values, packed as int8. `r` = RN(1 / step). The IEEE quotient comes
-// from two corrections of v r: the first residual correction leaves an error below one ulp, and
-// from such a quotient and a correctly rounded reciprocal the second gives RN(v / step) (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990). No step under-
-// or overflows: step is in [2^-24 / 127, 65504 / 127] and |v| is 0 or at least 2^-24.
+// rint(RN(v / step)) for eight values, packed as int8; step is in [2^-24 / 127, 65504 / 127].
 __device__ __forceinline__ uint2 row_codes(const uint4& v, float step, float r) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float2 md = make_float2(-step, -step), r2 = make_float2(r, r);
   uint32_t q[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = half2_bits_to_float2(w[j]);
-    const float fv[2] = {f.x, f.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float a = __fmul_rn(fv[i], r);
-      a = fmaf(fmaf(-step, a, fv[i]), r, a);
-      a = fmaf(fmaf(-step, a, fv[i]), r, a);
-      // |a| <= 127 (1 + 2^-23): adding 1.5 2^23 rounds half to even and leaves the integer in the low byte
-      q[2 * j + i] = __float_as_uint(a + 12582912.0f);
-    }
+    const float2 a = div_rn2(half2_bits_to_float2(w[j]), md, r2);
+    // |a| <= 127 (1 + 2^-23): adding 1.5 2^23 rounds half to even and leaves the integer in the low byte
+    q[2 * j] = __float_as_uint(a.x + 12582912.0f);
+    q[2 * j + 1] = __float_as_uint(a.y + 12582912.0f);
   }
   const uint32_t lo = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
   const uint32_t hi = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
