@@ -8,9 +8,10 @@
 //
 // The layer is bound by the packed weights of the experts that are chosen at all (0.52 bytes per
 // weight). One CTA per SM, launched cooperatively, in three phases with a grid-wide barrier between:
-//   0  the router's logits, a CTA per expert and 8 tokens; after the barrier every CTA picks all
+//   0  the router's logits, a CTA per expert and up to 8 tokens; after the barrier every CTA picks all
 //      tokens' experts itself and sorts the choices into blocks of at most 8 tokens of one expert;
-//   1  h for every unit (block, 16 gate rows and their 16 up rows);
+//   1  h for every unit (block, 16 gate rows and their 16 up rows), drawn a few at a time: SMs differ by
+//      up to 15% in the bandwidth they get;
 //   2  y for every 16-row output tile, summed over the blocks.
 // An expert with more than 8 tokens has several blocks, whose weights come from L2 after the first:
 // each block's activation fragments then fit a warp's registers.
@@ -27,6 +28,8 @@
 // that wait for it could otherwise hold the registers that its own last CTAs need, and the barrier
 // would never be complete.
 #pragma once
+
+#include <type_traits>
 
 #include "awq_common.cuh"
 #include "awq_gemm.cuh"
@@ -69,8 +72,8 @@ __host__ __device__ inline int moe_bufs(int T) { return T <= 16 ? 2 : 1; }
 // first slot; one more) take; then by slot the token, weight and expert.
 __host__ __device__ inline int moe_list_ints(int T, int top) { return 5 * T * top + 1; }
 __host__ __device__ inline int moe_smem_bytes(int T, int top) {
-  return kMoeStages * kMoeStage + moe_bufs(T) * kMoeCW * 2 * moe_rec_floats(T) * 4 + (2 * kMoeStages + 5) * 8 + 8 +
-         moe_list_ints(T, top) * 4;
+  return kMoeStages * kMoeStage + moe_bufs(T) * kMoeCW * 2 * moe_rec_floats(T) * 4 + (kMoeStages + 2) * 16 +
+         (2 * kMoeStages + 5) * 8 + 8 + moe_list_ints(T, top) * 4;
 }
 
 // How a strip (one tile of one block, Q group pairs along its K) is cut into stages. Up to 8 pairs:
@@ -93,6 +96,10 @@ struct MoeCut {
 __device__ unsigned long long g_moe_arrivals = 0;
 static_assert(kMoeStages * kMoeStage > 114 * 1024, "two of these CTAs must not fit one SM");
 
+// Tickets drawn for phase 1's units since the library was loaded. A launch reads the count before its
+// first barrier and draws after it, so all of its CTAs start from the same count.
+__device__ unsigned long long g_moe_tickets = 0;
+
 __device__ __forceinline__ unsigned long long moe_arrive() {
   unsigned long long old;
   asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(&g_moe_arrivals) : "memory");
@@ -111,6 +118,17 @@ __device__ __forceinline__ void moe_await(unsigned long long target, volatile in
   }
 }
 
+// A bounded wait whose common case, the phase complete at the first look or within one suspension, stays
+// small in the instruction stream.
+static __device__ __noinline__ bool moe_wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned long long budget) {
+  return mbar_wait_bounded(bar, parity, abort, budget);
+}
+__device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity, uint32_t hint, volatile int* abort,
+                                         unsigned long long budget) {
+  return mbar_try_wait_for(bar, parity, hint) || moe_wait_longer(bar, parity, abort, budget);
+}
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ uint4 ld_coherent_v4(const void* p) {
   uint4 v;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -124,31 +142,20 @@ template <int PER>
 __device__ __forceinline__ void moe_pick(const float* logits, int E, int top, bool renorm, int* ids, float* p) {
   const int lane = threadIdx.x & 31;
   uint32_t ord[PER];
-  float l[PER], best = -INFINITY;
+  float l[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = i * 32 + lane;
     ord[i] = 0;
     l[i] = -INFINITY;
-    if (e < E) {
-      asm volatile("ld.global.f32 %0, [%1];" : "=f"(l[i]) : "l"(logits + e));
-      const uint32_t b = __float_as_uint(l[i]);
-      ord[i] = l[i] != l[i] ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    }
+    if (e < E) asm volatile("ld.global.f32 %0, [%1];" : "=f"(l[i]) : "l"(logits + e));
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) best = fmaxf(best, l[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-  float total = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    l[i] = expf(l[i] - best);
-    if (i * 32 + lane < E) total += l[i];
+    const uint32_t b = __float_as_uint(l[i]);
+    if (i * 32 + lane < E) ord[i] = l[i] != l[i] ? 1u : (b & 0x80000000u) ? ~b : (b | 0x80000000u);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-  float mine = 0.0f, chosen = 0.0f;            // lane k: the k-th choice
+  float mine = 0.0f, best = 0.0f;              // lane k: the logit of the k-th choice
   int mine_id = 0;
   for (int k = 0; k < top; ++k) {
     uint32_t m = 0;
@@ -156,48 +163,42 @@ __device__ __forceinline__ void moe_pick(const float* logits, int E, int top, bo
     for (int i = 0; i < PER; ++i) m = max(m, ord[i]);
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     uint32_t e = 0xFFFFFFFFu;                  // the lowest index among the equal ones
-    float v = 0.0f;
 #pragma unroll
     for (int i = PER - 1; i >= 0; --i)
-      if (ord[i] == m) {
-        e = i * 32 + lane;
-        v = l[i];
-      }
-    const uint32_t first = __reduce_min_sync(0xFFFFFFFFu, e);
-    v = __shfl_sync(0xFFFFFFFFu, v, first & 31);
+      if (ord[i] == m) e = i * 32 + lane;
+    e = __reduce_min_sync(0xFFFFFFFFu, e);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (i * 32 + lane == static_cast<int>(first)) ord[i] = 0;
-    chosen += v;
-    if (lane == k) { mine = v; mine_id = static_cast<int>(first); }
+      if (i * 32 + lane == static_cast<int>(e)) ord[i] = 0;
+    const float v = m == 1u ? NAN : __uint_as_float((m & 0x80000000u) ? m ^ 0x80000000u : ~m);
+    if (k == 0) best = v;                      // the largest logit (NaN if all are)
+    if (lane == k) { mine = v; mine_id = static_cast<int>(e); }
   }
+  const float num = lane < top ? expf(mine - best) : 0.0f;
+  float total = num;
+  if (!renorm) {
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane < E) total += expf(l[i] - best);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if (lane < top) {
     ids[lane] = mine_id;
-    p[lane] = __fdiv_rn(mine, renorm ? chosen : total);
+    p[lane] = __fdiv_rn(num, total);
   }
 }
 
-// acc += S (sum x q) - S z (sum x) for the lane's four sums of one group (columns 2t, 2t+1 of rows r
-// and r+8), two columns to an instruction. tq carries 2^-24 (rows r) and 2^-20 (rows r+8).
-__device__ __forceinline__ void fma2(float2& d, float2 a, float2 b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;"
-      : "+l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-}
+// acc += S (sum x q - z sum x) for the lane's four sums of one group (columns 2t, 2t+1 of rows r and
+// r+8). tq carries 2^-24 in row r and 2^-20 in row r+8, and so does z as the bits of fp16 subnormals;
+// acc keeps those factors until the epilogue.
 __device__ __forceinline__ void moe_scale(float (&acc)[4], const float (&tq)[4], const float (&xs)[2], uint32_t sv, uint32_t zz) {
-  const float2 sf = half2_bits_to_float2(sv);
-  const float s_lo = sf.x * 16777216.0f, s_hi = sf.y * 1048576.0f;   // 2^24 and 2^20: exact
-  const float z_lo = -sf.x * small_uint_to_float(zz & 0xFu), z_hi = -sf.y * small_uint_to_float(zz >> 4);
-  float2 lo = make_float2(acc[0], acc[1]), hi = make_float2(acc[2], acc[3]);
-  const float2 x2 = make_float2(xs[0], xs[1]);
-  fma2(lo, make_float2(s_lo, s_lo), make_float2(tq[0], tq[1]));
-  fma2(hi, make_float2(s_hi, s_hi), make_float2(tq[2], tq[3]));
-  fma2(lo, make_float2(z_lo, z_lo), x2);
-  fma2(hi, make_float2(z_hi, z_hi), x2);
-  acc[0] = lo.x;
-  acc[1] = lo.y;
-  acc[2] = hi.x;
-  acc[3] = hi.y;
+  const float2 s = half2_bits_to_float2(sv), z = half2_bits_to_float2((zz * 0x10001u) & 0x00F0000Fu);
+  acc[0] = fmaf(s.x, fmaf(-z.x, xs[0], tq[0]), acc[0]);
+  acc[1] = fmaf(s.x, fmaf(-z.x, xs[1], tq[1]), acc[1]);
+  acc[2] = fmaf(s.y, fmaf(-z.y, xs[0], tq[2]), acc[2]);
+  acc[3] = fmaf(s.y, fmaf(-z.y, xs[1], tq[3]), acc[3]);
 }
 
 // The activation fragments of one group pair for one 8-token tile, and their sums per group.
@@ -237,7 +238,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   extern __shared__ __align__(128) uint8_t smem[];
   const int rec_floats = moe_rec_floats(a.T);
   float* rec = reinterpret_cast<float*>(smem + S * kMoeStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(rec + a.bufs * kMoeCW * 2 * rec_floats);
+  // what a stage or a record holds: block, first unit, units (0: the phase ends), then 2 * chunk + up tile
+  int4* stage_of = reinterpret_cast<int4*>(rec + a.bufs * kMoeCW * 2 * rec_floats);
+  int4* event_of = stage_of + S;
+  uint64_t* full = reinterpret_cast<uint64_t*>(event_of + 2);
   uint64_t* empty = full + S;
   uint64_t* rfull = empty + S;                 // record buffers
   uint64_t* rempty = rfull + 2;
@@ -269,46 +273,58 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   const unsigned long long budget = g_wait_budget_ns;
   const int c0 = blockIdx.x, nc = gridDim.x;
 
-  // ---- phase 0: logits of 8 tokens with one expert, the consumer warps splitting K
+  // ---- phase 0: logits of NT tokens with one expert, the consumer warps splitting K; as few tokens at a
+  // time as the CTAs allow
+  unsigned long long tickets = 0;
   {
+    if (threadIdx.x == 32 * kMoeCW)
+      asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(tickets) : "l"(&g_moe_tickets) : "memory");
     float* part = rec;                         // [2][kMoeCW][8]
-    const int tasks = a.E * ((a.T + 7) / 8);
-    for (int i = c0, it = 0; i < tasks; i += nc, it ^= 1) {
-      const int e = i % a.E, t0 = i / a.E * 8;
-      float acc[8] = {};
-      if (warp < kMoeCW) {
-        const __half* wr = a.router + static_cast<size_t>(e) * a.K;
-        for (int c = threadIdx.x; c < a.K / 8; c += 32 * kMoeCW) {
-          const uint4 wv = __ldg(reinterpret_cast<const uint4*>(wr + c * 8));
-          const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
+    auto logits = [&](auto n) {
+      constexpr int NT = decltype(n)::value;
+      const int tasks = a.E * ((a.T + NT - 1) / NT);
+      for (int i = c0, it = 0; i < tasks; i += nc, it ^= 1) {
+        const int e = i % a.E, t0 = i / a.E * NT;
+        if (warp < kMoeCW) {
+          const __half* wr = a.router + static_cast<size_t>(e) * a.K;
+          float acc[NT] = {};
+          for (int c = threadIdx.x; c < a.K / 8; c += 32 * kMoeCW) {
+            const uint4 wv = __ldg(reinterpret_cast<const uint4*>(wr + c * 8));
+            uint4 xv[NT];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            if (t0 + t >= a.T) break;
-            const uint4 xv = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(t0 + t) * a.K + c * 8));
-            const uint32_t x4[4] = {xv.x, xv.y, xv.z, xv.w};
+            for (int t = 0; t < NT; ++t)
+              xv[t] = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(min(t0 + t, a.T - 1)) * a.K + c * 8));
+            const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 wf = half2_bits_to_float2(w4[j]), xf = half2_bits_to_float2(x4[j]);
-              acc[t] = fmaf(wf.x, xf.x, acc[t]);
-              acc[t] = fmaf(wf.y, xf.y, acc[t]);
+            for (int t = 0; t < NT; ++t) {
+              const uint32_t x4[4] = {xv[t].x, xv[t].y, xv[t].z, xv[t].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 wf = half2_bits_to_float2(w4[j]), xf = half2_bits_to_float2(x4[j]);
+                acc[t] = fmaf(wf.x, xf.x, acc[t]);
+                acc[t] = fmaf(wf.y, xf.y, acc[t]);
+              }
             }
           }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
+            if (lane == 0) part[(it * kMoeCW + warp) * 8 + t] = acc[t];
+          }
         }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          if (t0 + t >= a.T) break;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
-          if (lane == 0) part[(it * kMoeCW + warp) * 8 + t] = acc[t];
+        __syncthreads();
+        if (threadIdx.x < NT && t0 + threadIdx.x < a.T) {
+          float v = 0.0f;
+          for (int w = 0; w < kMoeCW; ++w) v += part[(it * kMoeCW + w) * 8 + threadIdx.x];
+          a.logits[static_cast<size_t>(t0 + threadIdx.x) * a.E + e] = v;
         }
       }
-      __syncthreads();
-      if (threadIdx.x < 8 && t0 + threadIdx.x < a.T) {
-        float v = 0.0f;
-        for (int w = 0; w < kMoeCW; ++w) v += part[(it * kMoeCW + w) * 8 + threadIdx.x];
-        a.logits[static_cast<size_t>(t0 + threadIdx.x) * a.E + e] = v;
-      }
-    }
+    };
+    if (a.E * a.T <= nc) logits(std::integral_constant<int, 1>{});
+    else if (a.E * ((a.T + 1) / 2) <= nc) logits(std::integral_constant<int, 2>{});
+    else if (a.E * ((a.T + 3) / 4) <= nc) logits(std::integral_constant<int, 4>{});
+    else logits(std::integral_constant<int, 8>{});
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) moe_await(moe_arrive(), s_abort, budget);
@@ -352,13 +368,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   if (threadIdx.x == 0) l_first[V] = n_assign;
   __syncthreads();
 
-  // ---- this CTA's work; all roles walk the same stages in the same order
+  // ---- the work. Phase 1's units are drawn `grain` at a time by the producer, which leaves word of each
+  // stage's content beside it; phase 2's tiles are divided evenly.
   const int P = a.I / 16;
   const int G1 = a.K / kGroup, G2 = a.I / kGroup;
   const MoeCut k1((G1 + 1) / 2), k2((G2 + 1) / 2);
-  auto share = [&](int units, int c) { return static_cast<int>(static_cast<long long>(units) * c / nc); };
-  const int u1a = share(V * P, c0), u1b = share(V * P, c0 + 1);
-  const int u2a = share(a.K / 16, c0), u2b = share(a.K / 16, c0 + 1);
+  const int per = k1.strips == 1 ? 1 : k1.strips / 2;          // units of a stage (a stage pair with one strip)
+  const int grain = max(per, min(4, V * P / (8 * nc)));
+  const int u2a = static_cast<int>(static_cast<long long>(a.K / 16) * c0 / nc);
+  const int u2b = static_cast<int>(static_cast<long long>(a.K / 16) * (c0 + 1) / nc);
+  const uint32_t hint = static_cast<uint32_t>(min(budget, 1000000ull));
   int slot = 0;
   uint32_t phase = 0;
   auto advance = [&]() {
@@ -371,7 +390,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   };
   auto rec_of = [&](int w, int half) { return rec + ((rbuf * kMoeCW + w) * 2 + half) * rec_floats; };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, s_abort, budget));
+    return __all_sync(0xFFFFFFFFu, moe_wait(bar, parity, hint, s_abort, budget));
   };
 
   if (warp == kMoeCW) {
@@ -380,9 +399,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     int issued = 0;
     constexpr int kItem = kPairCodeBytes + kPairScaleBytes + kPairZeroBytes;
     uint8_t* sb = nullptr;
-    auto open = [&](int items) -> bool {
-      if (!mbar_wait_bounded(&empty[slot], phase ^ 1, s_abort, budget)) return false;
+    auto open = [&](int items, int4 what) -> bool {
+      if (!moe_wait(&empty[slot], phase ^ 1, hint, s_abort, budget)) return false;
       sb = smem + slot * kMoeStage;
+      stage_of[slot] = what;
       mbar_arrive_expect_tx(&full[slot], items * kItem);
       return true;
     };
@@ -399,38 +419,42 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     };
     const size_t gu_total = a.E * a.gu_pairs, dn_total = a.E * a.dn_pairs;
     auto produce = [&]() {
-      for (int u = u1a; u < u1b;) {
-        const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
-        const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
-        if (k1.strips == 1) {
-          for (int j0 = ja; j0 < jb; j0 += 2)
-            for (int c = 0; c < k1.chunks; ++c) {
-              const int p0 = c * k1.len, n = min(k1.len, k1.Q - p0);
-              for (int b = 0; b < 2 * min(2, jb - j0); ++b) {
-                if (!open(n)) return;
-                copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j0 + (b >> 1)) * k1.Q + p0, n, gu_total);
-                close();
-              }
+      const int units = V * P;
+      long long ticket = c0;
+      while (ticket * grain < units) {
+        unsigned long long drawn;              // the next one, asked for early
+        asm volatile("atom.add.relaxed.gpu.global.u64 %0, [%1], 1;" : "=l"(drawn) : "l"(&g_moe_tickets) : "memory");
+        const int end = min(units, static_cast<int>(ticket + 1) * grain);
+        for (int u = static_cast<int>(ticket) * grain; u < end;) {
+          const int x = u / P, j = u - x * P;
+          const int n = min(per, min(P - j, end - u));
+          const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
+          if (k1.strips == 1) {
+            for (int b = 0; b < 2 * k1.chunks; ++b) {
+              const int p0 = (b >> 1) * k1.len, m = min(k1.len, k1.Q - p0);
+              if (!open(m, make_int4(x, j, 1, b))) return;
+              copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j) * k1.Q + p0, m, gu_total);
+              close();
             }
-        } else {
-          const int half = k1.strips / 2;
-          for (int j0 = ja; j0 < jb; j0 += half) {
-            const int n = min(half, jb - j0) * k1.Q;
-            if (!open(2 * n)) return;
+          } else {
+            if (!open(2 * n * k1.Q, make_int4(x, j, n, 0))) return;
             for (int h = 0; h < 2; ++h)
-              copy(h * half * k1.Q, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>(h * P + j0) * k1.Q, n, gu_total);
+              copy(h * per * k1.Q, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>(h * P + j) * k1.Q, n * k1.Q, gu_total);
             close();
           }
+          u += n;
         }
-        u += jb - ja;
+        ticket = nc + static_cast<long long>(drawn - tickets);
       }
+      if (!open(0, make_int4(0, 0, 0, 0))) return;
+      close();
       for (int t0 = u2a; t0 < u2b; t0 += 2)
         for (int x0 = 0; x0 < V; x0 += k2.strips) {
           const int m = min(k2.strips, V - x0);
           for (int c = 0; c < k2.chunks; ++c) {
             const int p0 = c * k2.len, n = min(k2.len, k2.Q - p0);
             for (int b = 0; b < min(2, u2b - t0); ++b) {
-              if (!open(m * n)) return;
+              if (!open(m * n, make_int4(0, 0, 0, 0))) return;
               for (int i = 0; i < m; ++i)
                 copy(i * n, a.dn_q, a.dn_s, a.dn_z,
                      static_cast<size_t>(l_expert[x0 + i]) * a.dn_pairs + static_cast<size_t>(t0 + b) * k2.Q + p0, n, dn_total);
@@ -449,11 +473,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 
   if (warp == kMoeCW + 1) {
     // ---------------------------------------------------------------- epilogue warp
+    // the sum of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24, r + 8: 2^-20)
     auto sum = [&](int half, int w0, int nw, int col, int row) {
       float v = 0.0f;
 #pragma unroll 4
       for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
-      return v;
+      return v * (row < 8 ? 16777216.0f : 1048576.0f);
     };
     auto done = [&]() {
       __syncwarp();
@@ -461,28 +486,28 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       next_event();
     };
     bool ok = true;
-    for (int u = u1a; ok && u < u1b;) {
-      const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
-      const int first = l_first[x], cnt = l_first[x + 1] - first;
-      const int per = k1.strips == 1 ? 1 : k1.strips / 2;               // units per event
-      for (int j0 = ja; j0 < jb; j0 += per) {
-        ok = warp_wait(&rfull[rbuf], rphase);
-        if (!ok) break;
-        const int nu = min(per, jb - j0);
-        for (int q = lane; q < 16 * nu * cnt; q += 32) {
-          const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
-          const int i_row = 16 * (j0 + i) + row;
-          if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
-          const bool one = k1.strips == 1;
-          const float g = one ? sum(0, 0, k1.len, col, row) : sum(0, i * k1.wide, k1.Q, col, row);
-          const float v = one ? sum(1, 0, k1.len, col, row) : sum(0, (per + i) * k1.wide, k1.Q, col, row);
-          float hv = silu_mul(g, v) * l_p[first + col];
-          if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
-          a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
-        }
+    while (true) {
+      ok = warp_wait(&rfull[rbuf], rphase);
+      if (!ok) break;
+      const int4 what = event_of[rbuf];
+      const int x = what.x, nu = what.z;
+      if (nu == 0) {
         done();
+        break;
       }
-      u += jb - ja;
+      const int first = l_first[x], cnt = l_first[x + 1] - first;
+      for (int q = lane; q < 16 * nu * cnt; q += 32) {
+        const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
+        const int i_row = 16 * (what.y + i) + row;
+        if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
+        const bool one = k1.strips == 1;
+        const float g = one ? sum(0, 0, k1.len, col, row) : sum(0, i * k1.wide, k1.Q, col, row);
+        const float v = one ? sum(1, 0, k1.len, col, row) : sum(0, (per + i) * k1.wide, k1.Q, col, row);
+        float hv = silu_mul(g, v) * l_p[first + col];
+        if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
+        a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
+      }
+      done();
     }
     // every CTA's h is written (release) and visible (acquire)
     __threadfence();
@@ -550,6 +575,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       f.s[g][1] = d[1];
     }
   };
+  // Asks for the lines of pair `pr` of a block's tokens (a token per 4 lanes, 128 bytes a lane).
+  auto prefetch_frag = [&](const __half* row, int pr, int G) {
+    if (2 * pr + (t >> 1) < G) prefetch_l1(row + pr * 256 + t * 64);
+  };
   // Adds the products of the stage's item with the fragments.
   auto pair = [&](float (&acc)[4], const MoeFrag& f, int item) {
     const uint8_t* cb = sb + item * kPairCodeBytes + lane * 16;
@@ -565,59 +594,57 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 
   // ---- phase 1
   {
-    float acc[2][2][4] = {};
-    auto record = [&](float (&v)[4], int half) {
-      float* p = rec_of(warp, half) + 2 * t * 20 + r;
-      p[0] = v[0];
-      p[20] = v[1];
-      p[8] = v[2];
-      p[28] = v[3];
-      v[0] = v[1] = v[2] = v[3] = 0.0f;
-    };
+    float acc[4] = {}, other[4] = {};          // the stage's tile; the unit's other tile (several chunks)
     const int pl = warp % k1.wide, sub = warp / k1.wide;
     MoeFrag f;
-    for (int u = u1a; ok && u < u1b;) {
-      const int x = u / P, ja = u - x * P, jb = min(P, ja + u1b - u);
-      const int first = l_first[x], cnt = l_first[x + 1] - first;
-      // columns past the block's last token repeat it; they are never used
-      const __half* row = a.x + static_cast<size_t>(l_token[first + min(r, cnt - 1)]) * a.K;
-      if (k1.strips == 1) {
-        for (int j0 = ja; ok && j0 < jb; j0 += 2) {
-          const int nb = min(2, jb - j0);
-          for (int c = 0; ok && c < k1.chunks; ++c) {
-            const bool live = pl < min(k1.len, k1.Q - c * k1.len);
-            if (live && (k1.chunks > 1 || j0 == ja)) load_frag(f, row, c * k1.len + pl, G1);   // one chunk: once per block
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              if (b >= 2 * nb || !ok) break;
-              ok = take();
-              if (!ok) break;
-              if (live) pair(acc[b >> 1][b & 1], f, pl);
-              release();
-              if (c == k1.chunks - 1) {
-                if ((b & 1) == 0) ok = rec_ready();
-                if (!ok) break;
-                record(acc[b >> 1][b & 1], b & 1);
-                if (b & 1) rec_done();
-              }
-            }
-          }
-        }
-      } else {
-        const int half = k1.strips / 2, i = sub % half;
-        if (pl < k1.Q) load_frag(f, row, pl, G1);
-        for (int j0 = ja; ok && j0 < jb; j0 += half) {
-          ok = take();
-          if (!ok) break;
-          if (pl < k1.Q && j0 + i < jb) pair(acc[0][0], f, sub * k1.Q + pl);
-          release();
-          ok = rec_ready();
-          if (!ok) break;
-          record(acc[0][0], 0);
+    int fx = -1, fc = 0;                       // block and chunk of the fragments
+    while (true) {
+      ok = take();
+      if (!ok) break;
+      const int4 what = stage_of[slot];
+      const int x = what.x, c = what.w >> 1, half = what.w & 1;
+      if (what.z == 0) {                       // the phase ends
+        release();
+        ok = rec_ready();
+        if (!ok) break;
+        if (warp == 0 && lane == 0) event_of[rbuf] = what;
+        rec_done();
+        break;
+      }
+      const int pr = c * k1.len + pl;
+      const bool live = k1.strips == 1 ? pl < min(k1.len, k1.Q - c * k1.len) : pl < k1.Q && sub % per < what.z;
+      if (x != fx || c != fc) {
+        fx = x;
+        fc = c;
+        // columns past the block's last token repeat it; they are never used
+        const int first = l_first[x], cnt = l_first[x + 1] - first;
+        const __half* row = a.x + static_cast<size_t>(l_token[first + min(r, cnt - 1)]) * a.K;
+        if (pr < k1.Q) load_frag(f, row, pr, G1);
+      }
+      if (live) pair(acc, f, k1.strips == 1 ? pl : sub * k1.Q + pl);
+      release();
+      if (c == k1.chunks - 1) {                // the tile is complete
+        if (half == 0) ok = rec_ready();
+        if (!ok) break;
+        float* p = rec_of(warp, half) + 2 * t * 20 + r;
+        p[0] = acc[0];
+        p[20] = acc[1];
+        p[8] = acc[2];
+        p[28] = acc[3];
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+        if (k1.strips > 1 || half == 1) {
+          if (warp == 0 && lane == 0) event_of[rbuf] = what;
           rec_done();
         }
       }
-      u += jb - ja;
+      if (k1.chunks > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = acc[i];
+          acc[i] = other[i];
+          other[i] = v;
+        }
+      }
     }
   }
 
@@ -627,22 +654,32 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   {
     float acc[2][4] = {};
     const int pl = warp % k2.wide, sub = warp / k2.wide;
+    // the lane's activation row of block x, whose pairs this warp takes (null past the last block)
+    auto row_of = [&](int x) -> const __half* {
+      if (x >= V) return nullptr;
+      return a.h + static_cast<size_t>(min(l_first[x] + r, l_first[x + 1] - 1)) * a.I;
+    };
     for (int t0 = u2a; ok && t0 < u2b; t0 += 2) {
       const int nb = min(2, u2b - t0);
       ok = rec_ready();
       if (!ok) break;
       for (int i = lane; i < 2 * rec_floats; i += 32) rec_of(warp, 0)[i] = 0.0f;   // both halves
       __syncwarp();
+      const __half* row = row_of(sub);
+      if (row != nullptr && pl < k2.len) prefetch_frag(row, pl, G2);
       for (int x0 = 0; ok && x0 < V; x0 += k2.strips) {
         const int x = x0 + sub;
-        const bool mine = x < V;
-        const int first = mine ? l_first[x] : 0, cnt = mine ? l_first[x + 1] - first : 0;
-        const __half* row = a.h + static_cast<size_t>(first + max(0, min(r, cnt - 1))) * a.I;
+        const __half* next = row_of(x + k2.strips);
         for (int c = 0; ok && c < k2.chunks; ++c) {
-          const int n = min(k2.len, k2.Q - c * k2.len);
-          const bool live = mine && pl < n;
+          const int n = min(k2.len, k2.Q - c * k2.len), pr = c * k2.len + pl;
+          const bool live = row != nullptr && pl < n;
           MoeFrag f;
-          if (live) load_frag(f, row, c * k2.len + pl, G2);
+          if (live) load_frag(f, row, pr, G2);
+          if (c + 1 < k2.chunks) {             // what the warp reads next
+            if (row != nullptr && pr + k2.len < k2.Q) prefetch_frag(row, pr + k2.len, G2);
+          } else if (next != nullptr && pl < k2.len) {
+            prefetch_frag(next, pl, G2);
+          }
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             if (b >= nb || !ok) break;
@@ -653,7 +690,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
           }
         }
         if (!ok) break;
-        if (mine && pl < k2.len) {
+        if (row != nullptr && pl < k2.len) {
+          const int first = l_first[x], cnt = l_first[x + 1] - first;
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             if (2 * t + c < cnt) {
@@ -668,6 +706,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
         }
+        row = next;
       }
       if (ok) rec_done();
     }
