@@ -10,8 +10,8 @@
 // weight). One CTA per SM, launched cooperatively, in three phases with a grid-wide barrier between:
 //   0  the router's logits, a CTA per expert and up to 8 tokens; after the barrier every CTA picks all
 //      tokens' experts itself and sorts the choices into blocks of at most 8 tokens of one expert;
-//   1  h for every unit (block, 16 gate rows and their 16 up rows), drawn a few at a time: SMs differ by
-//      up to 15% in the bandwidth they get;
+//   1  h for every unit (block, 16 gate rows and their 16 up rows), the last of them drawn by whoever is
+//      done first: SMs differ by up to 15% in the bandwidth they get;
 //   2  y for every 16-row output tile, summed over the blocks.
 // An expert with more than 8 tokens has several blocks, whose weights come from L2 after the first:
 // each block's activation fragments then fit a warp's registers.
@@ -20,8 +20,8 @@
 // without waiting for the barrier, so phase 2's first weights arrive while phase 1 ends. A stage holds
 // 16 (tile, group pair) items, one for each of the 16 consumer warps, which so split a tile's K. A
 // warp's activation fragments stay in registers while it walks along the tiles of a block. Each warp
-// leaves its sums of a tile in shared memory, and an epilogue warp adds them in warp order and applies
-// SiLU, the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding
+// leaves its sums of a tile in shared memory, and epilogue warps add them in warp order and apply SiLU,
+// the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding
 // (2^-12 of each term on average) is the one that unfused layers make between their calls.
 //
 // The kernel neither starts before its predecessor has ended nor lets its successor start early: CTAs
@@ -55,7 +55,8 @@ struct MoeArgs {
 };
 
 constexpr int kMoeCW = 16;                      // consumer warps
-constexpr int kMoeThreads = 32 * (kMoeCW + 2);  // + producer, + epilogue
+constexpr int kMoeEpi = 3;                      // epilogue warps
+constexpr int kMoeThreads = 32 * (kMoeCW + 1 + kMoeEpi);   // + producer
 constexpr int kMoeStages = 4;
 constexpr int kMoeStageItems = 16;              // (tile, group pair) items per ring stage, one per consumer warp
 constexpr int kMoeOffS = kMoeStageItems * kPairCodeBytes;
@@ -73,11 +74,12 @@ __host__ __device__ inline int moe_bufs(int T) { return T <= 16 ? 2 : 1; }
 __host__ __device__ inline int moe_list_ints(int T, int top) { return 5 * T * top + 1; }
 __host__ __device__ inline int moe_smem_bytes(int T, int top) {
   return kMoeStages * kMoeStage + moe_bufs(T) * kMoeCW * 2 * moe_rec_floats(T) * 4 + (kMoeStages + 2) * 16 +
-         (2 * kMoeStages + 5) * 8 + 8 + moe_list_ints(T, top) * 4;
+         (2 * kMoeStages + 10) * 8 + 8 + moe_list_ints(T, top) * 4;
 }
 
 // How a strip (one tile of one block, Q group pairs along its K) is cut into stages. Up to 8 pairs:
-// `strips` strips share a stage, `wide` warps each. More: `chunks` stages of up to `len` pairs.
+// `strips` strips share a stage, `wide` warps each. More: `chunks` stages of up to `len` pairs. Stages
+// come in twos: the gate and the up tiles in phase 1, two output tiles in phase 2.
 struct MoeCut {
   int Q, wide, strips, chunks, len;
   __device__ explicit MoeCut(int q) : Q(q) {
@@ -127,7 +129,6 @@ __device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity, uint32_
                                          unsigned long long budget) {
   return mbar_try_wait_for(bar, parity, hint) || moe_wait_longer(bar, parity, abort, budget);
 }
-__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ uint4 ld_coherent_v4(const void* p) {
   uint4 v;
@@ -207,30 +208,43 @@ struct MoeFrag {
   float s[2][2];      // [group][column 2t, 2t+1]
 };
 
-// One group pair. A code pair masked out of its word is a pair of fp16 subnormals q 2^-24 (16 q 2^-24
-// in the odd nibbles, rows r+8): one AND makes an operand of the MMA, whose products are exact. The zero
-// point costs no instruction per code, it enters once per group with the group's activation sum. The
-// two groups' MMA chains run side by side.
-__device__ __forceinline__ void moe_pair(float (&acc)[4], const uint4 (&w)[2][2], const MoeFrag& f, const uint32_t (&sv)[2],
-                                         const uint32_t (&zz)[2]) {
-  float tq[2][4];
+// One group pair of N items (tiles) with the same fragments. A code pair masked out of its word is a pair
+// of fp16 subnormals q 2^-24 (16 q 2^-24 in the odd nibbles, rows r+8): one AND makes an operand of the
+// MMA, whose products are exact. The zero point costs no instruction per code, it enters once per group
+// with the group's activation sum. The 2 N MMA chains run side by side: a warp alone with two chains
+// leaves half of its time to the latency of shared memory and of the chain (two items at a time instead
+// of one: 8 tokens of the 4096 x 14336 layer 171 -> 150 us).
+template <int N>
+__device__ __forceinline__ void moe_pairs(float (&acc)[N][4], const uint8_t* const (&code)[N], const uint8_t* const (&scale)[N],
+                                          const uint8_t* const (&zero)[N], const MoeFrag& f) {
+  float tq[N][2][4];
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk)
+  for (int kk = 0; kk < 2; ++kk) {
+    uint4 w[N][2];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) w[i][g] = *reinterpret_cast<const uint4*>(code[i] + g * 1024 + kk * 512);
 #pragma unroll
     for (int s4 = 0; s4 < 4; ++s4)
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint4& wv = w[g][kk];
-        const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
-        const uint32_t q8 = q >> 8;
-        const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
-        const uint4& xq = f.v[g][kk][s4 >> 1];
-        const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
-        if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[g], a, b0, b1);
-        else mma_m16n8k16_f32(tq[g], a, b0, b1);
-      }
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-  for (int g = 0; g < 2; ++g) moe_scale(acc, tq[g], f.s[g], sv[g], zz[g]);
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t q = (s4 == 0) ? w[i][g].x : (s4 == 1) ? w[i][g].y : (s4 == 2) ? w[i][g].z : w[i][g].w;
+          const uint32_t q8 = q >> 8;
+          const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
+          const uint4& xq = f.v[g][kk][s4 >> 1];
+          const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
+          if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[i][g], a, b0, b1);
+          else mma_m16n8k16_f32(tq[i][g], a, b0, b1);
+        }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      moe_scale(acc[i], tq[i][g], f.s[g], *reinterpret_cast<const uint32_t*>(scale[i] + g * 32), zero[i][g * 8]);
 }
 
 __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a) {
@@ -238,14 +252,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   extern __shared__ __align__(128) uint8_t smem[];
   const int rec_floats = moe_rec_floats(a.T);
   float* rec = reinterpret_cast<float*>(smem + S * kMoeStage);
-  // what a stage or a record holds: block, first unit, units (0: the phase ends), then 2 * chunk + up tile
+  // what a stage or a record holds: block, first unit, units (0: the phase ends), chunk
   int4* stage_of = reinterpret_cast<int4*>(rec + a.bufs * kMoeCW * 2 * rec_floats);
   int4* event_of = stage_of + S;
   uint64_t* full = reinterpret_cast<uint64_t*>(event_of + 2);
   uint64_t* empty = full + S;
-  uint64_t* rfull = empty + S;                 // record buffers
+  uint64_t* rfull = empty + S;                 // record buffers, phase 1
   uint64_t* rempty = rfull + 2;
-  uint64_t* go = rempty + 2;                   // phase 2 may read h
+  uint64_t* tfull = rempty + 2;                // record buffers, phase 2
+  uint64_t* tempty = tfull + 2;
+  uint64_t* edone = tempty + 2;                // this CTA's h is stored
+  uint64_t* go = edone + 1;                    // phase 2 may read h
   volatile int* s_abort = reinterpret_cast<volatile int*>(go + 1);
   const int n_assign = a.T * a.top;
   int* l_ids = const_cast<int*>(s_abort) + 2;
@@ -264,8 +281,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&rfull[b], kMoeCW);
-      mbar_init(&rempty[b], 1);
+      mbar_init(&rempty[b], kMoeEpi);
+      mbar_init(&tfull[b], kMoeCW);
+      mbar_init(&tempty[b], kMoeCW);
     }
+    mbar_init(edone, kMoeEpi);
     mbar_init(go, 1);
     *s_abort = 0;
     mbar_fence_init();
@@ -368,13 +388,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   if (threadIdx.x == 0) l_first[V] = n_assign;
   __syncthreads();
 
-  // ---- the work. Phase 1's units are drawn `grain` at a time by the producer, which leaves word of each
-  // stage's content beside it; phase 2's tiles are divided evenly.
+  // ---- the work. Phase 1: the first units, all of them if they are few, are divided evenly; the last
+  // eighth of many goes to whoever is done first. The producer leaves word of each stage's content beside
+  // it. Phase 2: the tiles are divided evenly.
   const int P = a.I / 16;
   const int G1 = a.K / kGroup, G2 = a.I / kGroup;
   const MoeCut k1((G1 + 1) / 2), k2((G2 + 1) / 2);
-  const int per = k1.strips == 1 ? 1 : k1.strips / 2;          // units of a stage (a stage pair with one strip)
-  const int grain = max(per, min(4, V * P / (8 * nc)));
+  const int per = k1.strips;                   // units of a stage
   const int u2a = static_cast<int>(static_cast<long long>(a.K / 16) * c0 / nc);
   const int u2b = static_cast<int>(static_cast<long long>(a.K / 16) * (c0 + 1) / nc);
   const uint32_t hint = static_cast<uint32_t>(min(budget, 1000000ull));
@@ -419,32 +439,32 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     };
     const size_t gu_total = a.E * a.gu_pairs, dn_total = a.E * a.dn_pairs;
     auto produce = [&]() {
-      const int units = V * P;
-      long long ticket = c0;
-      while (ticket * grain < units) {
-        unsigned long long drawn;              // the next one, asked for early
-        asm volatile("atom.add.relaxed.gpu.global.u64 %0, [%1], 1;" : "=l"(drawn) : "l"(&g_moe_tickets) : "memory");
-        const int end = min(units, static_cast<int>(ticket + 1) * grain);
-        for (int u = static_cast<int>(ticket) * grain; u < end;) {
+      auto produce_units = [&](int u, int end) -> bool {
+        while (u < end) {
           const int x = u / P, j = u - x * P;
           const int n = min(per, min(P - j, end - u));
           const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
-          if (k1.strips == 1) {
-            for (int b = 0; b < 2 * k1.chunks; ++b) {
-              const int p0 = (b >> 1) * k1.len, m = min(k1.len, k1.Q - p0);
-              if (!open(m, make_int4(x, j, 1, b))) return;
-              copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j) * k1.Q + p0, m, gu_total);
-              close();
-            }
-          } else {
-            if (!open(2 * n * k1.Q, make_int4(x, j, n, 0))) return;
-            for (int h = 0; h < 2; ++h)
-              copy(h * per * k1.Q, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>(h * P + j) * k1.Q, n * k1.Q, gu_total);
+          for (int b = 0; b < 2 * k1.chunks; ++b) {
+            const int p0 = (b >> 1) * k1.len, m = min(k1.len, k1.Q - p0);   // n > 1: whole strips, one after another
+            if (!open(n * m, make_int4(x, j, n, b >> 1))) return false;
+            copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j) * k1.Q + p0, n * m, gu_total);
             close();
           }
           u += n;
         }
-        ticket = nc + static_cast<long long>(drawn - tickets);
+        return true;
+      };
+      const int units = V * P;
+      const int even = units < 8 * nc * per ? units : units - units / 8;
+      if (!produce_units(static_cast<int>(static_cast<long long>(even) * c0 / nc),
+                         static_cast<int>(static_cast<long long>(even) * (c0 + 1) / nc)))
+        return;
+      while (even < units) {                   // the ring holds several stages while a draw takes its time
+        unsigned long long drawn;
+        asm volatile("atom.add.relaxed.gpu.global.u64 %0, [%1], 1;" : "=l"(drawn) : "l"(&g_moe_tickets) : "memory");
+        const long long u = even + static_cast<long long>(drawn - tickets) * per;
+        if (u >= units) break;
+        if (!produce_units(static_cast<int>(u), static_cast<int>(min(u + per, static_cast<long long>(units))))) return;
       }
       if (!open(0, make_int4(0, 0, 0, 0))) return;
       close();
@@ -471,15 +491,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     return;
   }
 
-  if (warp == kMoeCW + 1) {
-    // ---------------------------------------------------------------- epilogue warp
-    // the sum of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24, r + 8: 2^-20)
-    auto sum = [&](int half, int w0, int nw, int col, int row) {
-      float v = 0.0f;
-#pragma unroll 4
-      for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
-      return v * (row < 8 ? 16777216.0f : 1048576.0f);
-    };
+  // The sum of the records of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24,
+  // row r + 8: 2^-20).
+  auto sum = [&](int half, int w0, int nw, int col, int row) {
+    float v = 0.0f;
+#pragma unroll 8
+    for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
+    return v * (row < 8 ? 16777216.0f : 1048576.0f);
+  };
+
+  if (warp > kMoeCW) {
+    // ---------------------------------------------------------------- epilogue warps (phase 1)
     auto done = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&rempty[rbuf]);
@@ -496,52 +518,44 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         break;
       }
       const int first = l_first[x], cnt = l_first[x + 1] - first;
-      for (int q = lane; q < 16 * nu * cnt; q += 32) {
+      for (int q = 32 * (warp - kMoeCW - 1) + lane; q < 16 * nu * cnt; q += 32 * kMoeEpi) {
         const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
         const int i_row = 16 * (what.y + i) + row;
         if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
-        const bool one = k1.strips == 1;
-        const float g = one ? sum(0, 0, k1.len, col, row) : sum(0, i * k1.wide, k1.Q, col, row);
-        const float v = one ? sum(1, 0, k1.len, col, row) : sum(0, (per + i) * k1.wide, k1.Q, col, row);
+        const float g = sum(0, i * k1.wide, k1.len, col, row), v = sum(1, i * k1.wide, k1.len, col, row);
         float hv = silu_mul(g, v) * l_p[first + col];
         if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
         a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
       }
       done();
     }
-    // every CTA's h is written (release) and visible (acquire)
+    // the grid-wide barrier: every CTA's h is written (release) and visible (acquire)
     __threadfence();
     __syncwarp();
-    if (lane == 0) {
-      moe_await(moe_arrive(), s_abort, budget);
-      if (*s_abort == 0) mbar_arrive(go);
-    }
-    __syncwarp();   // the other lanes block here: polling ahead, they could keep lane 0 from its turn
-    for (int t0 = u2a; ok && t0 < u2b; t0 += 2) {
-      ok = warp_wait(&rfull[rbuf], rphase);
-      if (!ok) break;
-      const int rows = 16 * min(2, u2b - t0);
-      for (int q = lane; q < rows * a.T; q += 32) {
-        const int row = q % rows, col = q / rows;
-        if (!AWQ_CHECK(16 * t0 + row < a.K)) continue;
-        a.y[static_cast<size_t>(col) * a.K + 16 * t0 + row] = __float2half_rn(sum(row >> 4, 0, kMoeCW, col, row & 15));
+    if (lane == 0) mbar_arrive(edone);
+    if (warp == kMoeCW + 1) {
+      warp_wait(edone, 0);
+      if (lane == 0) {
+        moe_await(moe_arrive(), s_abort, budget);
+        if (*s_abort == 0) mbar_arrive(go);
       }
-      done();
+      __syncwarp();
     }
     return;
   }
 
   // ------------------------------------------------------------------ consumer warps
   const int r = lane >> 2, t = lane & 3;
-  const uint8_t* sb = nullptr;
-  auto take = [&]() -> bool {
-    sb = smem + slot * kMoeStage;
-    return warp_wait(&full[slot], phase);
+  auto take = [&]() -> bool { return warp_wait(&full[slot], phase); };
+  auto take_second = [&]() -> bool {           // the stage after the current one
+    return slot + 1 == S ? warp_wait(&full[0], phase ^ 1) : warp_wait(&full[slot + 1], phase);
   };
-  auto release = [&]() {
+  auto release = [&](int n) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[slot]);
-    advance();
+    for (int i = 0; i < n; ++i) {
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      advance();
+    }
   };
   auto rec_ready = [&]() { return warp_wait(&rempty[rbuf], rphase ^ 1); };
   auto rec_done = [&]() {
@@ -575,26 +589,29 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       f.s[g][1] = d[1];
     }
   };
-  // Asks for the lines of pair `pr` of a block's tokens (a token per 4 lanes, 128 bytes a lane).
-  auto prefetch_frag = [&](const __half* row, int pr, int G) {
-    if (2 * pr + (t >> 1) < G) prefetch_l1(row + pr * 256 + t * 64);
+  // Adds the products of an item of the current stage, or of the same item of this one and the next.
+  auto one = [&](float (&acc)[1][4], const MoeFrag& f, int item) {
+    const uint8_t* sb = smem + slot * kMoeStage;
+    const uint8_t* const code[1] = {sb + item * kPairCodeBytes + lane * 16};
+    const uint8_t* const scale[1] = {sb + kMoeOffS + item * kPairScaleBytes + r * 4};
+    const uint8_t* const zero[1] = {sb + kMoeOffZ + item * kPairZeroBytes + r};
+    moe_pairs<1>(acc, code, scale, zero, f);
   };
-  // Adds the products of the stage's item with the fragments.
-  auto pair = [&](float (&acc)[4], const MoeFrag& f, int item) {
-    const uint8_t* cb = sb + item * kPairCodeBytes + lane * 16;
-    const uint8_t* sc = sb + kMoeOffS + item * kPairScaleBytes + r * 4;
-    const uint8_t* zb = sb + kMoeOffZ + item * kPairZeroBytes + r;
-    const uint4 w[2][2] = {{*reinterpret_cast<const uint4*>(cb), *reinterpret_cast<const uint4*>(cb + 512)},
-                           {*reinterpret_cast<const uint4*>(cb + 1024), *reinterpret_cast<const uint4*>(cb + 1536)}};
-    const uint32_t sv[2] = {*reinterpret_cast<const uint32_t*>(sc), *reinterpret_cast<const uint32_t*>(sc + 32)};
-    const uint32_t zz[2] = {zb[0], zb[8]};
-    moe_pair(acc, w, f, sv, zz);
+  auto two = [&](float (&acc)[2][4], const MoeFrag& f, int item) {
+    const uint8_t* sb = smem + slot * kMoeStage;
+    const uint8_t* sc = slot + 1 == S ? smem : sb + kMoeStage;
+    const int oc = item * kPairCodeBytes + lane * 16, os = kMoeOffS + item * kPairScaleBytes + r * 4,
+              oz = kMoeOffZ + item * kPairZeroBytes + r;
+    const uint8_t* const code[2] = {sb + oc, sc + oc};
+    const uint8_t* const scale[2] = {sb + os, sc + os};
+    const uint8_t* const zero[2] = {sb + oz, sc + oz};
+    moe_pairs<2>(acc, code, scale, zero, f);
   };
   bool ok = true;
 
   // ---- phase 1
   {
-    float acc[4] = {}, other[4] = {};          // the stage's tile; the unit's other tile (several chunks)
+    float acc[2][4] = {};                      // gate and up tile
     const int pl = warp % k1.wide, sub = warp / k1.wide;
     MoeFrag f;
     int fx = -1, fc = 0;                       // block and chunk of the fragments
@@ -602,9 +619,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       ok = take();
       if (!ok) break;
       const int4 what = stage_of[slot];
-      const int x = what.x, c = what.w >> 1, half = what.w & 1;
+      const int x = what.x, c = what.w;
       if (what.z == 0) {                       // the phase ends
-        release();
+        release(1);
         ok = rec_ready();
         if (!ok) break;
         if (warp == 0 && lane == 0) event_of[rbuf] = what;
@@ -612,103 +629,103 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         break;
       }
       const int pr = c * k1.len + pl;
-      const bool live = k1.strips == 1 ? pl < min(k1.len, k1.Q - c * k1.len) : pl < k1.Q && sub % per < what.z;
       if (x != fx || c != fc) {
         fx = x;
         fc = c;
         // columns past the block's last token repeat it; they are never used
         const int first = l_first[x], cnt = l_first[x + 1] - first;
         const __half* row = a.x + static_cast<size_t>(l_token[first + min(r, cnt - 1)]) * a.K;
-        if (pr < k1.Q) load_frag(f, row, pr, G1);
+        if (pl < k1.len && pr < k1.Q) load_frag(f, row, pr, G1);
       }
-      if (live) pair(acc, f, k1.strips == 1 ? pl : sub * k1.Q + pl);
-      release();
-      if (c == k1.chunks - 1) {                // the tile is complete
-        if (half == 0) ok = rec_ready();
+      ok = take_second();
+      if (!ok) break;
+      if (pl < k1.len && pr < k1.Q && sub < what.z) two(acc, f, sub * k1.Q + pl);
+      release(2);
+      if (c == k1.chunks - 1) {                // the unit is complete
+        ok = rec_ready();
         if (!ok) break;
-        float* p = rec_of(warp, half) + 2 * t * 20 + r;
-        p[0] = acc[0];
-        p[20] = acc[1];
-        p[8] = acc[2];
-        p[28] = acc[3];
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-        if (k1.strips > 1 || half == 1) {
-          if (warp == 0 && lane == 0) event_of[rbuf] = what;
-          rec_done();
-        }
-      }
-      if (k1.chunks > 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = acc[i];
-          acc[i] = other[i];
-          other[i] = v;
+        for (int h = 0; h < 2; ++h) {
+          float* p = rec_of(warp, h) + 2 * t * 20 + r;
+          p[0] = acc[h][0];
+          p[20] = acc[h][1];
+          p[8] = acc[h][2];
+          p[28] = acc[h][3];
+          acc[h][0] = acc[h][1] = acc[h][2] = acc[h][3] = 0.0f;
         }
+        if (warp == 0 && lane == 0) event_of[rbuf] = what;
+        rec_done();
       }
     }
   }
 
+  // (every record of phase 1 has been read: the barrier comes after the last event's h)
   ok = ok && warp_wait(go, 0);
 
   // ---- phase 2: a block's sums are added to its tokens' places in the warp's record
   {
     float acc[2][4] = {};
     const int pl = warp % k2.wide, sub = warp / k2.wide;
-    // the lane's activation row of block x, whose pairs this warp takes (null past the last block)
-    auto row_of = [&](int x) -> const __half* {
-      if (x >= V) return nullptr;
-      return a.h + static_cast<size_t>(min(l_first[x] + r, l_first[x + 1] - 1)) * a.I;
-    };
+    rbuf = 0;
+    rphase = 0;
     for (int t0 = u2a; ok && t0 < u2b; t0 += 2) {
       const int nb = min(2, u2b - t0);
-      ok = rec_ready();
+      ok = warp_wait(&tempty[rbuf], rphase ^ 1);
       if (!ok) break;
       for (int i = lane; i < 2 * rec_floats; i += 32) rec_of(warp, 0)[i] = 0.0f;   // both halves
       __syncwarp();
-      const __half* row = row_of(sub);
-      if (row != nullptr && pl < k2.len) prefetch_frag(row, pl, G2);
       for (int x0 = 0; ok && x0 < V; x0 += k2.strips) {
         const int x = x0 + sub;
-        const __half* next = row_of(x + k2.strips);
+        const bool mine = x < V && pl < k2.len;
+        const int first = mine ? l_first[x] : 0, cnt = mine ? l_first[x + 1] - first : 1;
+        const __half* row = a.h + static_cast<size_t>(first + min(r, cnt - 1)) * a.I;
         for (int c = 0; ok && c < k2.chunks; ++c) {
-          const int n = min(k2.len, k2.Q - c * k2.len), pr = c * k2.len + pl;
-          const bool live = row != nullptr && pl < n;
+          const int n = min(k2.len, k2.Q - c * k2.len);
+          const bool live = mine && pl < n;
           MoeFrag f;
-          if (live) load_frag(f, row, pr, G2);
-          if (c + 1 < k2.chunks) {             // what the warp reads next
-            if (row != nullptr && pr + k2.len < k2.Q) prefetch_frag(row, pr + k2.len, G2);
-          } else if (next != nullptr && pl < k2.len) {
-            prefetch_frag(next, pl, G2);
-          }
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (b >= nb || !ok) break;
-            ok = take();
+          if (live) load_frag(f, row, c * k2.len + pl, G2);
+          ok = take();
+          if (!ok) break;
+          if (nb == 2) {
+            ok = take_second();
             if (!ok) break;
-            if (live) pair(acc[b], f, sub * n + pl);
-            release();
+            if (live) two(acc, f, sub * n + pl);
+          } else if (live) {
+            one(reinterpret_cast<float(&)[1][4]>(acc), f, sub * n + pl);
           }
+          release(nb);
         }
         if (!ok) break;
-        if (row != nullptr && pl < k2.len) {
-          const int first = l_first[x], cnt = l_first[x + 1] - first;
+        if (mine) {
 #pragma unroll
           for (int c = 0; c < 2; ++c)
             if (2 * t + c < cnt) {
               float* p = rec_of(warp, 0) + l_token[first + 2 * t + c] * 20 + r;
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                if (b >= nb) break;
-                p[b * rec_floats] += acc[b][c];
-                p[b * rec_floats + 8] += acc[b][c + 2];
+              p[0] += acc[0][c];
+              p[8] += acc[0][c + 2];
+              if (nb == 2) {
+                p[rec_floats] += acc[1][c];
+                p[rec_floats + 8] += acc[1][c + 2];
               }
             }
 #pragma unroll
           for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
         }
-        row = next;
       }
-      if (ok) rec_done();
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tfull[rbuf]);
+      ok = warp_wait(&tfull[rbuf], rphase);
+      if (!ok) break;
+      for (int q = threadIdx.x; q < 16 * nb * a.T; q += 32 * kMoeCW) {
+        const int row = q & 15, b = (q >> 4) % nb, col = (q >> 4) / nb;
+        const int k = 16 * (t0 + b) + row;
+        if (!AWQ_CHECK(k < a.K)) continue;
+        a.y[static_cast<size_t>(col) * a.K + k] = __float2half_rn(sum(b, 0, kMoeCW, col, row));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[rbuf]);
+      next_event();
     }
   }
 }
