@@ -351,7 +351,7 @@ AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residu
  *           do not matter. Calls that may overlap on the GPU need workspaces of their own.
  * Only the chosen experts' weights are read. A logit that is NaN ranks below every number.
  * One kernel, a cooperative launch with one CTA on every SM that waits (bounded, AWQ_ERR_TIMEOUT) for
- * all others after the router and between the two layers. Bitwise reproducible.
+ * all others after the router and after each of the two layers. Bitwise reproducible.
  * Requires 1 <= T <= 32, 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I multiples of 128, each
  * expert's layers within awq_*_bytes' limits; every pointer 16-byte aligned. */
 AWQ_API size_t awq_moe_workspace_bytes(int T, int E, int K, int I, int top_k);

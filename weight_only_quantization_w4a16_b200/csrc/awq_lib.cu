@@ -741,15 +741,18 @@ inline bool search_shape_ok(int M, int N, int K) {
 
 
 // --------------------------------------------------------------------------- mixture of experts
-// Workspace: the router's logits and the intermediate h, each piece 256-byte aligned.
+// Workspace: the router's logits, the intermediate h and the down layers' partial sums, each piece
+// 256-byte aligned.
 struct MoeWs {
-  size_t logits, h, total;
+  size_t logits, h, part, total;
 };
-MoeWs moe_ws(int T, int E, int I, int top) {
+MoeWs moe_ws(int T, int E, int K, int I, int top) {
   MoeWs w{};
+  const size_t slots = static_cast<size_t>(T) * top;
   size_t o = 0;
   w.logits = o; o = align256(o + static_cast<size_t>(T) * E * 4);
-  w.h = o; o = align256(o + static_cast<size_t>(T) * top * I * 2);
+  w.h = o; o = align256(o + slots * I * 2);
+  w.part = o; o = align256(o + slots * MoeCut((I / kGroup + 1) / 2).chunks * K * 4);
   w.total = o;
   return w;
 }
@@ -1149,7 +1152,7 @@ awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, cons
 }
 
 size_t awq_moe_workspace_bytes(int T, int E, int K, int I, int top_k) {
-  return moe_shape_ok(T, E, K, I, top_k) ? moe_ws(T, E, I, top_k).total : 0;
+  return moe_shape_ok(T, E, K, I, top_k) ? moe_ws(T, E, K, I, top_k).total : 0;
 }
 
 awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint32_t* gate_up_qweight,
@@ -1161,7 +1164,7 @@ awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint
       !down_zeros || !y || !workspace)
     return AWQ_ERR_INVALID_ARG;
   if (!moe_shape_ok(T, E, K, I, top_k)) return AWQ_ERR_INVALID_ARG;
-  const MoeWs w = moe_ws(T, E, I, top_k);
+  const MoeWs w = moe_ws(T, E, K, I, top_k);
   if (workspace_bytes < w.total) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(router) || !aligned16(gate_up_qweight) || !aligned16(gate_up_scales) ||
       !aligned16(gate_up_zeros) || !aligned16(down_qweight) || !aligned16(down_scales) || !aligned16(down_zeros) ||
@@ -1186,10 +1189,10 @@ awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint
   a.router = reinterpret_cast<const __half*>(router);
   a.logits = reinterpret_cast<float*>(ws + w.logits);
   a.h = reinterpret_cast<__half*>(ws + w.h);
+  a.part = reinterpret_cast<float*>(ws + w.part);
   a.y = reinterpret_cast<__half*>(y);
   a.T = T; a.E = E; a.K = K; a.I = I; a.top = top_k;
   a.renorm = renormalize != 0;
-  a.bufs = moe_bufs(T);
   static std::atomic<uint64_t> smem_done{0};
   if ((st = ensure_smem(awq_moe_kernel, 227 * 1024, dev, smem_done)) != AWQ_OK) return st;
   return launch_attr(awq_moe_kernel, dim3(static_cast<unsigned>(sms), 1, 1), dim3(kMoeThreads, 1, 1), dim3(0, 0, 0), true,

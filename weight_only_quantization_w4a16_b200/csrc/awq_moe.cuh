@@ -7,22 +7,25 @@
 //   y_t  = sum over the chosen e of h . Wd_e^T
 //
 // The layer is bound by the packed weights of the experts that are chosen at all (0.52 bytes per
-// weight). One CTA per SM, launched cooperatively, in three phases with a grid-wide barrier between:
+// weight). One CTA per SM, launched cooperatively, in four phases with a grid-wide barrier between:
 //   0  the router's logits, a CTA per expert and up to 8 tokens; after the barrier every CTA picks all
 //      tokens' experts itself and sorts the choices into blocks of at most 8 tokens of one expert;
-//   1  h for every unit (block, 16 gate rows and their 16 up rows), the last of them drawn by whoever is
-//      done first: SMs differ by up to 15% in the bandwidth they get;
-//   2  y for every 16-row output tile, summed over the blocks.
-// An expert with more than 8 tokens has several blocks, whose weights come from L2 after the first:
-// each block's activation fragments then fit a warp's registers.
+//   1  h for every unit (block, 16 gate rows and their 16 up rows);
+//   2  fp32 partial sums of y for every unit (block, part of K, two 16-row output tiles);
+//   3  y, the partial sums added in a fixed order.
+// In phases 1 and 2 the last units go to whoever is done first: SMs differ by up to 15% in the bandwidth
+// they get. An expert with more than 8 tokens has several blocks, whose weights come from L2 after the
+// first: each block's activation fragments then fit a warp's registers. Phase 2 goes through partial
+// sums so that its units are as many and as small as phase 1's and a warp keeps its fragments along the
+// tiles; summing all blocks of a tile in one CTA left it at 59% of the HBM rate where phase 1 has 87%.
 //
 // Per CTA: a producer lane streams both phases' packed weights through one ring of shared memory
 // without waiting for the barrier, so phase 2's first weights arrive while phase 1 ends. A stage holds
 // 16 (tile, group pair) items, one for each of the 16 consumer warps, which so split a tile's K. A
 // warp's activation fragments stay in registers while it walks along the tiles of a block. Each warp
 // leaves its sums of a tile in shared memory, and epilogue warps add them in warp order and apply SiLU,
-// the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding
-// (2^-12 of each term on average) is the one that unfused layers make between their calls.
+// the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding (2^-12 of
+// each term on average) is the one that unfused layers make between their calls.
 //
 // The kernel neither starts before its predecessor has ended nor lets its successor start early: CTAs
 // that wait for it could otherwise hold the registers that its own last CTAs need, and the barrier
@@ -49,9 +52,9 @@ struct MoeArgs {
   const float* h_scale;                        // [E, I] or null
   float* logits;                               // [T, E]
   __half* h;                                   // [T * top, I]
+  float* part;                                 // [T * top, chunks of I, K]
   __half* y;                                   // [T, K]
   int T, E, K, I, top, renorm;
-  int bufs;                                    // record buffers
 };
 
 constexpr int kMoeCW = 16;                      // consumer warps
@@ -65,16 +68,15 @@ constexpr int kMoeStage = kMoeOffZ + kMoeStageItems * kPairZeroBytes;   // 34048
 static_assert(kMoeStage % 128 == 0, "ring stages stay aligned");
 
 // A record is one warp's fp32 sums of one 16-row tile, [column][20] (20: rows padded so that the
-// fragment stores hit distinct banks): a block's 8 columns in phase 1, the T tokens in phase 2.
-// A buffer holds two tiles' records of every warp; two buffers while they leave room for the ring.
-__host__ __device__ inline int moe_rec_floats(int T) { return (T < 8 ? 8 : T) * 20; }
-__host__ __device__ inline int moe_bufs(int T) { return T <= 16 ? 2 : 1; }
+// fragment stores hit distinct banks). A buffer holds two tiles' records of every warp.
+constexpr int kMoeRec = 8 * 20;
+constexpr int kMoeBufs = 2;
 // Routing lists: the choices in (token, rank) order (expert, weight), whose place the blocks (expert,
-// first slot; one more) take; then by slot the token, weight and expert.
-__host__ __device__ inline int moe_list_ints(int T, int top) { return 5 * T * top + 1; }
+// first slot; one more) take; then by slot the token, weight and expert; and the choices' slots.
+__host__ __device__ inline int moe_list_ints(int T, int top) { return 6 * T * top + 1; }
 __host__ __device__ inline int moe_smem_bytes(int T, int top) {
-  return kMoeStages * kMoeStage + moe_bufs(T) * kMoeCW * 2 * moe_rec_floats(T) * 4 + (kMoeStages + 2) * 16 +
-         (2 * kMoeStages + 10) * 8 + 8 + moe_list_ints(T, top) * 4;
+  return kMoeStages * kMoeStage + kMoeBufs * kMoeCW * 2 * kMoeRec * 4 + (kMoeStages + kMoeBufs) * 16 +
+         (2 * kMoeStages + 2 * kMoeBufs + 2) * 8 + 8 + moe_list_ints(T, top) * 4;
 }
 
 // How a strip (one tile of one block, Q group pairs along its K) is cut into stages. Up to 8 pairs:
@@ -82,7 +84,7 @@ __host__ __device__ inline int moe_smem_bytes(int T, int top) {
 // come in twos: the gate and the up tiles in phase 1, two output tiles in phase 2.
 struct MoeCut {
   int Q, wide, strips, chunks, len;
-  __device__ explicit MoeCut(int q) : Q(q) {
+  __host__ __device__ explicit MoeCut(int q) : Q(q) {
     wide = q <= 1 ? 1 : q <= 2 ? 2 : q <= 4 ? 4 : q <= 8 ? 8 : 16;
     strips = kMoeStageItems / wide;
     chunks = (q + kMoeStageItems - 1) / kMoeStageItems;
@@ -98,9 +100,9 @@ struct MoeCut {
 __device__ unsigned long long g_moe_arrivals = 0;
 static_assert(kMoeStages * kMoeStage > 114 * 1024, "two of these CTAs must not fit one SM");
 
-// Tickets drawn for phase 1's units since the library was loaded. A launch reads the count before its
-// first barrier and draws after it, so all of its CTAs start from the same count.
-__device__ unsigned long long g_moe_tickets = 0;
+// Tickets drawn for the units of phases 1 and 2 since the library was loaded. A launch reads the counts
+// before its first barrier and draws after it, so all of its CTAs start from the same counts.
+__device__ __align__(16) unsigned long long g_moe_tickets[2] = {0, 0};
 
 __device__ __forceinline__ unsigned long long moe_arrive() {
   unsigned long long old;
@@ -250,19 +252,16 @@ __device__ __forceinline__ void moe_pairs(float (&acc)[N][4], const uint8_t* con
 __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a) {
   constexpr int S = kMoeStages;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int rec_floats = moe_rec_floats(a.T);
   float* rec = reinterpret_cast<float*>(smem + S * kMoeStage);
   // what a stage or a record holds: block, first unit, units (0: the phase ends), chunk
-  int4* stage_of = reinterpret_cast<int4*>(rec + a.bufs * kMoeCW * 2 * rec_floats);
+  int4* stage_of = reinterpret_cast<int4*>(rec + kMoeBufs * kMoeCW * 2 * kMoeRec);
   int4* event_of = stage_of + S;
-  uint64_t* full = reinterpret_cast<uint64_t*>(event_of + 2);
+  uint64_t* full = reinterpret_cast<uint64_t*>(event_of + kMoeBufs);
   uint64_t* empty = full + S;
-  uint64_t* rfull = empty + S;                 // record buffers, phase 1
-  uint64_t* rempty = rfull + 2;
-  uint64_t* tfull = rempty + 2;                // record buffers, phase 2
-  uint64_t* tempty = tfull + 2;
-  uint64_t* edone = tempty + 2;                // this CTA's h is stored
-  uint64_t* go = edone + 1;                    // phase 2 may read h
+  uint64_t* rfull = empty + S;                 // record buffers
+  uint64_t* rempty = rfull + kMoeBufs;
+  uint64_t* edone = rempty + kMoeBufs;         // this CTA's results of the phase are stored
+  uint64_t* go = edone + 1;                    // everybody's are
   volatile int* s_abort = reinterpret_cast<volatile int*>(go + 1);
   const int n_assign = a.T * a.top;
   int* l_ids = const_cast<int*>(s_abort) + 2;
@@ -272,6 +271,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   int* l_token = l_first + n_assign + 1;
   float* l_p = reinterpret_cast<float*>(l_token + n_assign);
   int* l_slot = reinterpret_cast<int*>(l_p + n_assign);        // expert of a slot, times two, + 1 where a block starts
+  int* l_of = l_slot + n_assign;               // slot of a choice
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -279,11 +279,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kMoeCW);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kMoeBufs; ++b) {
       mbar_init(&rfull[b], kMoeCW);
       mbar_init(&rempty[b], kMoeEpi);
-      mbar_init(&tfull[b], kMoeCW);
-      mbar_init(&tempty[b], kMoeCW);
     }
     mbar_init(edone, kMoeEpi);
     mbar_init(go, 1);
@@ -295,10 +293,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 
   // ---- phase 0: logits of NT tokens with one expert, the consumer warps splitting K; as few tokens at a
   // time as the CTAs allow
-  unsigned long long tickets = 0;
+  unsigned long long tickets[2] = {0, 0};
   {
     if (threadIdx.x == 32 * kMoeCW)
-      asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(tickets) : "l"(&g_moe_tickets) : "memory");
+      asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];"
+                   : "=l"(tickets[0]), "=l"(tickets[1])
+                   : "l"(&g_moe_tickets)
+                   : "memory");
     float* part = rec;                         // [2][kMoeCW][8]
     auto logits = [&](auto n) {
       constexpr int NT = decltype(n)::value;
@@ -372,6 +373,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     l_token[first + rank] = i / a.top;
     l_p[first + rank] = l_pa[i];
     l_slot[first + rank] = 2 * e + (rank % 8 == 0);
+    l_of[i] = first + rank;
   }
   __syncthreads();
   int V = 0;                                   // blocks
@@ -388,15 +390,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   if (threadIdx.x == 0) l_first[V] = n_assign;
   __syncthreads();
 
-  // ---- the work. Phase 1: the first units, all of them if they are few, are divided evenly; the last
-  // eighth of many goes to whoever is done first. The producer leaves word of each stage's content beside
-  // it. Phase 2: the tiles are divided evenly.
-  const int P = a.I / 16;
-  const int G1 = a.K / kGroup, G2 = a.I / kGroup;
-  const MoeCut k1((G1 + 1) / 2), k2((G2 + 1) / 2);
-  const int per = k1.strips;                   // units of a stage
-  const int u2a = static_cast<int>(static_cast<long long>(a.K / 16) * c0 / nc);
-  const int u2b = static_cast<int>(static_cast<long long>(a.K / 16) * (c0 + 1) / nc);
+  // ---- phases 1 and 2. A unit is the items of two tiles, j and j + P (gate and up; the two halves of
+  // y). In phase 2 every chunk of K has units of its own. The first units, all of them if they are few,
+  // are divided evenly, and the last eighth of many is drawn. The producer leaves word of each stage's
+  // content beside it, from which the others learn what to do.
+  const MoeCut k1((a.K / kGroup + 1) / 2), k2((a.I / kGroup + 1) / 2);
   const uint32_t hint = static_cast<uint32_t>(min(budget, 1000000ull));
   int slot = 0;
   uint32_t phase = 0;
@@ -406,9 +404,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   int rbuf = 0;                                // record buffer of the current event
   uint32_t rphase = 0;
   auto next_event = [&]() {
-    if (++rbuf == a.bufs) { rbuf = 0; rphase ^= 1; }
+    if (++rbuf == kMoeBufs) { rbuf = 0; rphase ^= 1; }
   };
-  auto rec_of = [&](int w, int half) { return rec + ((rbuf * kMoeCW + w) * 2 + half) * rec_floats; };
+  auto rec_of = [&](int w, int half) { return rec + ((rbuf * kMoeCW + w) * 2 + half) * kMoeRec; };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, moe_wait(bar, parity, hint, s_abort, budget));
   };
@@ -418,72 +416,56 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     if (lane != 0) return;
     int issued = 0;
     constexpr int kItem = kPairCodeBytes + kPairScaleBytes + kPairZeroBytes;
-    uint8_t* sb = nullptr;
-    auto open = [&](int items, int4 what) -> bool {
-      if (!moe_wait(&empty[slot], phase ^ 1, hint, s_abort, budget)) return false;
-      sb = smem + slot * kMoeStage;
-      stage_of[slot] = what;
-      mbar_arrive_expect_tx(&full[slot], items * kItem);
-      return true;
-    };
-    // `n` items from (tile, pair) index tp of the packed layers into places at..at+n-1 of the stage
-    auto copy = [&](int at, const uint8_t* q, const uint8_t* s, const uint8_t* z, size_t tp, int n, size_t total) {
-      if (!AWQ_CHECK(n >= 1 && at >= 0 && at + n <= kMoeStageItems && tp + n <= total)) return;
-      bulk_g2s(sb + at * kPairCodeBytes, q + tp * kPairCodeBytes, n * kPairCodeBytes, &full[slot]);
-      bulk_g2s(sb + kMoeOffS + at * kPairScaleBytes, s + tp * kPairScaleBytes, n * kPairScaleBytes, &full[slot]);
-      bulk_g2s(sb + kMoeOffZ + at * kPairZeroBytes, z + tp * kPairZeroBytes, n * kPairZeroBytes, &full[slot]);
-    };
-    auto close = [&]() {
-      ++issued;
-      advance();
-    };
-    const size_t gu_total = a.E * a.gu_pairs, dn_total = a.E * a.dn_pairs;
-    auto produce = [&]() {
-      auto produce_units = [&](int u, int end) -> bool {
+    auto produce = [&](bool second) -> bool {
+      const MoeCut& k = second ? k2 : k1;
+      const uint8_t *q = second ? a.dn_q : a.gu_q, *sc = second ? a.dn_s : a.gu_s, *z = second ? a.dn_z : a.gu_z;
+      const size_t pairs = second ? a.dn_pairs : a.gu_pairs, total = a.E * pairs;
+      const int P = second ? a.K / 32 : a.I / 16;
+      auto stage = [&](int4 what, int half) -> bool {          // `what.z` units' tiles of one half
+        if (!moe_wait(&empty[slot], phase ^ 1, hint, s_abort, budget)) return false;
+        uint8_t* sb = smem + slot * kMoeStage;
+        const int p0 = what.w * k.len, n = what.z * min(k.len, k.Q - p0);
+        stage_of[slot] = what;
+        mbar_arrive_expect_tx(&full[slot], n * kItem);
+        if (n > 0) {
+          const size_t tp = static_cast<size_t>(l_expert[what.x]) * pairs + static_cast<size_t>(half * P + what.y) * k.Q + p0;
+          if (AWQ_CHECK(n <= kMoeStageItems && tp + n <= total)) {
+            bulk_g2s(sb, q + tp * kPairCodeBytes, n * kPairCodeBytes, &full[slot]);
+            bulk_g2s(sb + kMoeOffS, sc + tp * kPairScaleBytes, n * kPairScaleBytes, &full[slot]);
+            bulk_g2s(sb + kMoeOffZ, z + tp * kPairZeroBytes, n * kPairZeroBytes, &full[slot]);
+          }
+        }
+        ++issued;
+        advance();
+        return true;
+      };
+      auto units = [&](int u, int end) -> bool {
         while (u < end) {
-          const int x = u / P, j = u - x * P;
-          const int n = min(per, min(P - j, end - u));
-          const size_t base = static_cast<size_t>(l_expert[x]) * a.gu_pairs;
-          for (int b = 0; b < 2 * k1.chunks; ++b) {
-            const int p0 = (b >> 1) * k1.len, m = min(k1.len, k1.Q - p0);   // n > 1: whole strips, one after another
-            if (!open(n * m, make_int4(x, j, n, b >> 1))) return false;
-            copy(0, a.gu_q, a.gu_s, a.gu_z, base + static_cast<size_t>((b & 1) * P + j) * k1.Q + p0, n * m, gu_total);
-            close();
+          const int v = u / P, j = u - v * P;
+          const int x = second ? v / k.chunks : v, n = min(k.strips, min(P - j, end - u));
+          for (int c = second ? v - x * k.chunks : 0;; ++c) {
+            if (!stage(make_int4(x, j, n, c), 0) || !stage(make_int4(x, j, n, c), 1)) return false;
+            if (second || c + 1 == k.chunks) break;
           }
           u += n;
         }
         return true;
       };
-      const int units = V * P;
-      const int even = units < 8 * nc * per ? units : units - units / 8;
-      if (!produce_units(static_cast<int>(static_cast<long long>(even) * c0 / nc),
-                         static_cast<int>(static_cast<long long>(even) * (c0 + 1) / nc)))
-        return;
-      while (even < units) {                   // the ring holds several stages while a draw takes its time
+      const int all = (second ? V * k.chunks : V) * P;
+      const int even = all < 8 * nc * k.strips ? all : all - all / 8;
+      if (!units(static_cast<int>(static_cast<long long>(even) * c0 / nc),
+                 static_cast<int>(static_cast<long long>(even) * (c0 + 1) / nc)))
+        return false;
+      while (even < all) {                     // the ring holds several stages while a draw takes its time
         unsigned long long drawn;
-        asm volatile("atom.add.relaxed.gpu.global.u64 %0, [%1], 1;" : "=l"(drawn) : "l"(&g_moe_tickets) : "memory");
-        const long long u = even + static_cast<long long>(drawn - tickets) * per;
-        if (u >= units) break;
-        if (!produce_units(static_cast<int>(u), static_cast<int>(min(u + per, static_cast<long long>(units))))) return;
+        asm volatile("atom.add.relaxed.gpu.global.u64 %0, [%1], 1;" : "=l"(drawn) : "l"(&g_moe_tickets[second]) : "memory");
+        const long long u = even + static_cast<long long>(drawn - (second ? tickets[1] : tickets[0])) * k.strips;
+        if (u >= all) break;
+        if (!units(static_cast<int>(u), static_cast<int>(min(u + k.strips, static_cast<long long>(all))))) return false;
       }
-      if (!open(0, make_int4(0, 0, 0, 0))) return;
-      close();
-      for (int t0 = u2a; t0 < u2b; t0 += 2)
-        for (int x0 = 0; x0 < V; x0 += k2.strips) {
-          const int m = min(k2.strips, V - x0);
-          for (int c = 0; c < k2.chunks; ++c) {
-            const int p0 = c * k2.len, n = min(k2.len, k2.Q - p0);
-            for (int b = 0; b < min(2, u2b - t0); ++b) {
-              if (!open(m * n, make_int4(0, 0, 0, 0))) return;
-              for (int i = 0; i < m; ++i)
-                copy(i * n, a.dn_q, a.dn_s, a.dn_z,
-                     static_cast<size_t>(l_expert[x0 + i]) * a.dn_pairs + static_cast<size_t>(t0 + b) * k2.Q + p0, n, dn_total);
-              close();
-            }
-          }
-        }
+      return stage(make_int4(0, 0, 0, 0), 0);  // the phase ends
     };
-    produce();
+    if (produce(false)) produce(true);
     // drain: every copy this thread issued has landed before the CTA may exit
     int never = 0;
     for (int i = max(0, issued - S); i < issued; ++i)
@@ -491,77 +473,75 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     return;
   }
 
-  // The sum of the records of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24,
-  // row r + 8: 2^-20).
-  auto sum = [&](int half, int w0, int nw, int col, int row) {
-    float v = 0.0f;
-#pragma unroll 8
-    for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
-    return v * (row < 8 ? 16777216.0f : 1048576.0f);
-  };
-
   if (warp > kMoeCW) {
-    // ---------------------------------------------------------------- epilogue warps (phase 1)
-    auto done = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rempty[rbuf]);
-      next_event();
+    // ---------------------------------------------------------------- epilogue warps
+    // the sum of the records of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24,
+    // row r + 8: 2^-20)
+    auto sum = [&](int half, int w0, int nw, int col, int row) {
+      float v = 0.0f;
+#pragma unroll 8
+      for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
+      return v * (row < 8 ? 16777216.0f : 1048576.0f);
     };
+    const int lane0 = 32 * (warp - kMoeCW - 1) + lane;
     bool ok = true;
-    while (true) {
-      ok = warp_wait(&rfull[rbuf], rphase);
-      if (!ok) break;
-      const int4 what = event_of[rbuf];
-      const int x = what.x, nu = what.z;
-      if (nu == 0) {
-        done();
-        break;
+    for (int ph = 0; ph < 2; ++ph) {
+      while (ok) {
+        ok = warp_wait(&rfull[rbuf], rphase);
+        if (!ok) break;
+        const int4 what = event_of[rbuf];
+        const int x = what.x, nu = what.z;
+        if (nu > 0) {
+          const int first = l_first[x], cnt = l_first[x + 1] - first;
+          if (ph == 0) {
+            for (int q = lane0; q < 16 * nu * cnt; q += 32 * kMoeEpi) {
+              const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
+              const int i_row = 16 * (what.y + i) + row;
+              if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
+              const float g = sum(0, i * k1.wide, k1.len, col, row), v = sum(1, i * k1.wide, k1.len, col, row);
+              float hv = silu_mul(g, v) * l_p[first + col];
+              if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
+              a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
+            }
+          } else {
+            const int nw = min(k2.len, k2.Q - what.w * k2.len);
+            for (int q = lane0; q < 32 * nu * cnt; q += 32 * kMoeEpi) {
+              const int row = q & 15, i = (q >> 4) % nu, half = (q >> 4) / nu & 1, col = (q >> 5) / nu;
+              const int k = 16 * (half * (a.K / 32) + what.y + i) + row;
+              if (!AWQ_CHECK(first + col < n_assign && k < a.K)) continue;
+              a.part[(static_cast<size_t>(first + col) * k2.chunks + what.w) * a.K + k] = sum(half, i * k2.wide, nw, col, row);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rempty[rbuf]);
+        next_event();
+        if (nu == 0) break;
       }
-      const int first = l_first[x], cnt = l_first[x + 1] - first;
-      for (int q = 32 * (warp - kMoeCW - 1) + lane; q < 16 * nu * cnt; q += 32 * kMoeEpi) {
-        const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
-        const int i_row = 16 * (what.y + i) + row;
-        if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
-        const float g = sum(0, i * k1.wide, k1.len, col, row), v = sum(1, i * k1.wide, k1.len, col, row);
-        float hv = silu_mul(g, v) * l_p[first + col];
-        if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
-        a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
-      }
-      done();
-    }
-    // the grid-wide barrier: every CTA's h is written (release) and visible (acquire)
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(edone);
-    if (warp == kMoeCW + 1) {
-      warp_wait(edone, 0);
-      if (lane == 0) {
-        moe_await(moe_arrive(), s_abort, budget);
-        if (*s_abort == 0) mbar_arrive(go);
-      }
+      // the grid-wide barrier: every CTA's results are written (release) and visible (acquire)
+      __threadfence();
       __syncwarp();
+      if (lane == 0) mbar_arrive(edone);
+      if (warp == kMoeCW + 1) {
+        warp_wait(edone, ph);
+        if (lane == 0) {
+          moe_await(moe_arrive(), s_abort, budget);
+          if (*s_abort == 0) mbar_arrive(go);
+        }
+        __syncwarp();   // the other lanes block here: polling ahead, they could keep lane 0 from its turn
+      }
     }
     return;
   }
 
   // ------------------------------------------------------------------ consumer warps
   const int r = lane >> 2, t = lane & 3;
-  auto take = [&]() -> bool { return warp_wait(&full[slot], phase); };
-  auto take_second = [&]() -> bool {           // the stage after the current one
-    return slot + 1 == S ? warp_wait(&full[0], phase ^ 1) : warp_wait(&full[slot + 1], phase);
-  };
   auto release = [&](int n) {
     __syncwarp();
     for (int i = 0; i < n; ++i) {
       if (lane == 0) mbar_arrive(&empty[slot]);
       advance();
     }
-  };
-  auto rec_ready = [&]() { return warp_wait(&rempty[rbuf], rphase ^ 1); };
-  auto rec_done = [&]() {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&rfull[rbuf]);
-    next_event();
   };
   // The fragments of pair `pr` for a block's tokens, and their sums; `row` is the lane's token.
   auto load_frag = [&](MoeFrag& f, const __half* row, int pr, int G) {
@@ -589,144 +569,85 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       f.s[g][1] = d[1];
     }
   };
-  // Adds the products of an item of the current stage, or of the same item of this one and the next.
-  auto one = [&](float (&acc)[1][4], const MoeFrag& f, int item) {
-    const uint8_t* sb = smem + slot * kMoeStage;
-    const uint8_t* const code[1] = {sb + item * kPairCodeBytes + lane * 16};
-    const uint8_t* const scale[1] = {sb + kMoeOffS + item * kPairScaleBytes + r * 4};
-    const uint8_t* const zero[1] = {sb + kMoeOffZ + item * kPairZeroBytes + r};
-    moe_pairs<1>(acc, code, scale, zero, f);
-  };
-  auto two = [&](float (&acc)[2][4], const MoeFrag& f, int item) {
-    const uint8_t* sb = smem + slot * kMoeStage;
-    const uint8_t* sc = slot + 1 == S ? smem : sb + kMoeStage;
-    const int oc = item * kPairCodeBytes + lane * 16, os = kMoeOffS + item * kPairScaleBytes + r * 4,
-              oz = kMoeOffZ + item * kPairZeroBytes + r;
-    const uint8_t* const code[2] = {sb + oc, sc + oc};
-    const uint8_t* const scale[2] = {sb + os, sc + os};
-    const uint8_t* const zero[2] = {sb + oz, sc + oz};
-    moe_pairs<2>(acc, code, scale, zero, f);
-  };
   bool ok = true;
-
-  // ---- phase 1
-  {
-    float acc[2][4] = {};                      // gate and up tile
-    const int pl = warp % k1.wide, sub = warp / k1.wide;
+  for (int ph = 0; ph < 2; ++ph) {
+    const MoeCut& k = ph ? k2 : k1;
+    const int G = (ph ? a.I : a.K) / kGroup;
+    const int pl = warp % k.wide, sub = warp / k.wide;
+    float acc[2][4] = {};                      // the unit's two tiles
     MoeFrag f;
     int fx = -1, fc = 0;                       // block and chunk of the fragments
-    while (true) {
-      ok = take();
+    while (ok) {
+      ok = warp_wait(&full[slot], phase);
       if (!ok) break;
       const int4 what = stage_of[slot];
       const int x = what.x, c = what.w;
-      if (what.z == 0) {                       // the phase ends
-        release(1);
-        ok = rec_ready();
-        if (!ok) break;
-        if (warp == 0 && lane == 0) event_of[rbuf] = what;
-        rec_done();
-        break;
-      }
-      const int pr = c * k1.len + pl;
-      if (x != fx || c != fc) {
-        fx = x;
-        fc = c;
-        // columns past the block's last token repeat it; they are never used
-        const int first = l_first[x], cnt = l_first[x + 1] - first;
-        const __half* row = a.x + static_cast<size_t>(l_token[first + min(r, cnt - 1)]) * a.K;
-        if (pl < k1.len && pr < k1.Q) load_frag(f, row, pr, G1);
-      }
-      ok = take_second();
-      if (!ok) break;
-      if (pl < k1.len && pr < k1.Q && sub < what.z) two(acc, f, sub * k1.Q + pl);
-      release(2);
-      if (c == k1.chunks - 1) {                // the unit is complete
-        ok = rec_ready();
-        if (!ok) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float* p = rec_of(warp, h) + 2 * t * 20 + r;
-          p[0] = acc[h][0];
-          p[20] = acc[h][1];
-          p[8] = acc[h][2];
-          p[28] = acc[h][3];
-          acc[h][0] = acc[h][1] = acc[h][2] = acc[h][3] = 0.0f;
+      if (what.z > 0) {
+        const int pr = c * k.len + pl;
+        const bool mine = pl < k.len && pr < k.Q;
+        if (x != fx || c != fc) {
+          fx = x;
+          fc = c;
+          // columns past the block's last token repeat it; they are never used
+          const int first = l_first[x], s = first + min(r, l_first[x + 1] - first - 1);
+          const __half* row = ph ? a.h + static_cast<size_t>(s) * a.I : a.x + static_cast<size_t>(l_token[s]) * a.K;
+          if (mine) load_frag(f, row, pr, G);
         }
-        if (warp == 0 && lane == 0) event_of[rbuf] = what;
-        rec_done();
+        const int next = slot + 1 == S ? 0 : slot + 1;         // the other half's stage
+        ok = warp_wait(&full[next], next == 0 ? phase ^ 1 : phase);
+        if (!ok) break;
+        if (mine && sub < what.z) {
+          const int item = sub * k.Q + pl;     // several strips: one after another
+          const uint8_t *s0 = smem + slot * kMoeStage, *s1 = smem + next * kMoeStage;
+          const int oc = item * kPairCodeBytes + lane * 16, os = kMoeOffS + item * kPairScaleBytes + r * 4,
+                    oz = kMoeOffZ + item * kPairZeroBytes + r;
+          const uint8_t* const code[2] = {s0 + oc, s1 + oc};
+          const uint8_t* const scale[2] = {s0 + os, s1 + os};
+          const uint8_t* const zero[2] = {s0 + oz, s1 + oz};
+          moe_pairs<2>(acc, code, scale, zero, f);
+        }
       }
+      release(what.z > 0 ? 2 : 1);
+      if (ph == 0 && what.z > 0 && c + 1 < k.chunks) continue;   // the unit's sums go on
+      ok = warp_wait(&rempty[rbuf], rphase ^ 1);
+      if (!ok) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float* p = rec_of(warp, h) + 2 * t * 20 + r;
+        p[0] = acc[h][0];
+        p[20] = acc[h][1];
+        p[8] = acc[h][2];
+        p[28] = acc[h][3];
+        acc[h][0] = acc[h][1] = acc[h][2] = acc[h][3] = 0.0f;
+      }
+      if (warp == 0 && lane == 0) event_of[rbuf] = what;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rfull[rbuf]);
+      next_event();
+      if (what.z == 0) break;
     }
+    ok = ok && warp_wait(go, ph);
   }
 
-  // (every record of phase 1 has been read: the barrier comes after the last event's h)
-  ok = ok && warp_wait(go, 0);
-
-  // ---- phase 2: a block's sums are added to its tokens' places in the warp's record
-  {
-    float acc[2][4] = {};
-    const int pl = warp % k2.wide, sub = warp / k2.wide;
-    rbuf = 0;
-    rphase = 0;
-    for (int t0 = u2a; ok && t0 < u2b; t0 += 2) {
-      const int nb = min(2, u2b - t0);
-      ok = warp_wait(&tempty[rbuf], rphase ^ 1);
-      if (!ok) break;
-      for (int i = lane; i < 2 * rec_floats; i += 32) rec_of(warp, 0)[i] = 0.0f;   // both halves
-      __syncwarp();
-      for (int x0 = 0; ok && x0 < V; x0 += k2.strips) {
-        const int x = x0 + sub;
-        const bool mine = x < V && pl < k2.len;
-        const int first = mine ? l_first[x] : 0, cnt = mine ? l_first[x + 1] - first : 1;
-        const __half* row = a.h + static_cast<size_t>(first + min(r, cnt - 1)) * a.I;
-        for (int c = 0; ok && c < k2.chunks; ++c) {
-          const int n = min(k2.len, k2.Q - c * k2.len);
-          const bool live = mine && pl < n;
-          MoeFrag f;
-          if (live) load_frag(f, row, c * k2.len + pl, G2);
-          ok = take();
-          if (!ok) break;
-          if (nb == 2) {
-            ok = take_second();
-            if (!ok) break;
-            if (live) two(acc, f, sub * n + pl);
-          } else if (live) {
-            one(reinterpret_cast<float(&)[1][4]>(acc), f, sub * n + pl);
-          }
-          release(nb);
-        }
-        if (!ok) break;
-        if (mine) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (2 * t + c < cnt) {
-              float* p = rec_of(warp, 0) + l_token[first + 2 * t + c] * 20 + r;
-              p[0] += acc[0][c];
-              p[8] += acc[0][c + 2];
-              if (nb == 2) {
-                p[rec_floats] += acc[1][c];
-                p[rec_floats + 8] += acc[1][c + 2];
-              }
-            }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] = 0.0f;
-        }
+  // ---- phase 3: y, four values a thread; a token's partial sums in the order of its choices and of K
+  if (!ok) return;
+  const int quads = a.K / 4;
+  for (int q = c0 * 32 * kMoeCW + threadIdx.x; q < a.T * quads; q += nc * 32 * kMoeCW) {
+    const int tok = q / quads, k4 = (q - tok * quads) * 4;
+    float v[4] = {};
+    for (int i = 0; i < a.top; ++i) {
+      const float* p = a.part + static_cast<size_t>(l_of[tok * a.top + i]) * k2.chunks * a.K + k4;
+      for (int c = 0; c < k2.chunks; ++c) {
+        const uint4 w = ld_coherent_v4(p + static_cast<size_t>(c) * a.K);
+        v[0] += __uint_as_float(w.x);
+        v[1] += __uint_as_float(w.y);
+        v[2] += __uint_as_float(w.z);
+        v[3] += __uint_as_float(w.w);
       }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tfull[rbuf]);
-      ok = warp_wait(&tfull[rbuf], rphase);
-      if (!ok) break;
-      for (int q = threadIdx.x; q < 16 * nb * a.T; q += 32 * kMoeCW) {
-        const int row = q & 15, b = (q >> 4) % nb, col = (q >> 4) / nb;
-        const int k = 16 * (t0 + b) + row;
-        if (!AWQ_CHECK(k < a.K)) continue;
-        a.y[static_cast<size_t>(col) * a.K + k] = __float2half_rn(sum(b, 0, kMoeCW, col, row));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[rbuf]);
-      next_event();
     }
+    const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(a.y + static_cast<size_t>(tok) * a.K + k4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
 }
 
