@@ -21,8 +21,9 @@
 //
 // Per CTA: a producer lane streams both phases' packed weights through one ring of shared memory
 // without waiting for the barrier, so phase 2's first weights arrive while phase 1 ends. A stage holds
-// 16 (tile, group pair) items, one for each of the 16 consumer warps, which so split a tile's K. A
-// warp's activation fragments stay in registers while it walks along the tiles of a block. Each warp
+// 16 (tile, group pair) items of each of two tiles, one of each for each of the 16 consumer warps, which so
+// split the tiles' K. A warp's activation fragments stay in registers while it walks along the tiles of a
+// block. Each warp
 // leaves its sums of a tile in shared memory, and epilogue warps add them in warp order and apply SiLU,
 // the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding (2^-12 of
 // each term on average) is the one that unfused layers make between their calls.
@@ -60,11 +61,11 @@ struct MoeArgs {
 constexpr int kMoeCW = 16;                      // consumer warps
 constexpr int kMoeEpi = 3;                      // epilogue warps
 constexpr int kMoeThreads = 32 * (kMoeCW + 1 + kMoeEpi);   // + producer
-constexpr int kMoeStages = 4;
-constexpr int kMoeStageItems = 16;              // (tile, group pair) items per ring stage, one per consumer warp
-constexpr int kMoeOffS = kMoeStageItems * kPairCodeBytes;
-constexpr int kMoeOffZ = kMoeOffS + kMoeStageItems * kPairScaleBytes;
-constexpr int kMoeStage = kMoeOffZ + kMoeStageItems * kPairZeroBytes;   // 34048 bytes
+constexpr int kMoeStages = 2;
+constexpr int kMoeTile = 16;                    // (tile, group pair) items of a stage's half, one per consumer warp
+constexpr int kMoeOffS = 2 * kMoeTile * kPairCodeBytes;
+constexpr int kMoeOffZ = kMoeOffS + 2 * kMoeTile * kPairScaleBytes;
+constexpr int kMoeStage = kMoeOffZ + 2 * kMoeTile * kPairZeroBytes;     // 68096 bytes
 static_assert(kMoeStage % 128 == 0, "ring stages stay aligned");
 
 // A record is one warp's fp32 sums of one 16-row tile, [column][20] (20: rows padded so that the
@@ -80,14 +81,14 @@ __host__ __device__ inline int moe_smem_bytes(int T, int top) {
 }
 
 // How a strip (one tile of one block, Q group pairs along its K) is cut into stages. Up to 8 pairs:
-// `strips` strips share a stage, `wide` warps each. More: `chunks` stages of up to `len` pairs. Stages
-// come in twos: the gate and the up tiles in phase 1, two output tiles in phase 2.
+// 2^shift strips share a stage's half, `wide` warps each. More: `chunks` stages of up to `len` pairs.
 struct MoeCut {
-  int Q, wide, strips, chunks, len;
+  int Q, wide, shift, strips, chunks, len;
   __host__ __device__ explicit MoeCut(int q) : Q(q) {
-    wide = q <= 1 ? 1 : q <= 2 ? 2 : q <= 4 ? 4 : q <= 8 ? 8 : 16;
-    strips = kMoeStageItems / wide;
-    chunks = (q + kMoeStageItems - 1) / kMoeStageItems;
+    shift = q <= 1 ? 4 : q <= 2 ? 3 : q <= 4 ? 2 : q <= 8 ? 1 : 0;
+    strips = 1 << shift;
+    wide = kMoeTile >> shift;
+    chunks = (q + kMoeTile - 1) / kMoeTile;
     len = (q + chunks - 1) / chunks;
   }
 };
@@ -104,6 +105,8 @@ static_assert(kMoeStages * kMoeStage > 114 * 1024, "two of these CTAs must not f
 // before its first barrier and draws after it, so all of its CTAs start from the same counts.
 __device__ __align__(16) unsigned long long g_moe_tickets[2] = {0, 0};
 
+// The arrival releases, at GPU scope, what the thread has written or seen synchronised from its CTA's
+// other threads, and the wait acquires it, so a CTA barrier on either side completes the chain.
 __device__ __forceinline__ unsigned long long moe_arrive() {
   unsigned long long old;
   asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], 1;" : "=l"(old) : "l"(&g_moe_arrivals) : "memory");
@@ -210,50 +213,43 @@ struct MoeFrag {
   float s[2][2];      // [group][column 2t, 2t+1]
 };
 
-// One group pair of N items (tiles) with the same fragments. A code pair masked out of its word is a pair
-// of fp16 subnormals q 2^-24 (16 q 2^-24 in the odd nibbles, rows r+8): one AND makes an operand of the
-// MMA, whose products are exact. The zero point costs no instruction per code, it enters once per group
-// with the group's activation sum. The 2 N MMA chains run side by side: a warp alone with two chains
-// leaves half of its time to the latency of shared memory and of the chain (two items at a time instead
-// of one: 8 tokens of the 4096 x 14336 layer 171 -> 150 us).
-template <int N>
-__device__ __forceinline__ void moe_pairs(float (&acc)[N][4], const uint8_t* const (&code)[N], const uint8_t* const (&scale)[N],
-                                          const uint8_t* const (&zero)[N], const MoeFrag& f) {
-  float tq[N][2][4];
+// The codes, scales and zero points of one item, in registers: the stage can be refilled while the
+// products are computed.
+struct MoeItem {
+  uint4 w[2][2];      // [group][64-k tile]
+  uint32_t s[2], z[2];
+};
+
+// acc += the item's products with the fragments. A code pair masked out of its word is a pair of fp16
+// subnormals q 2^-24 (16 q 2^-24 in the odd nibbles, rows r+8): one AND makes an operand of the MMA, whose
+// products are exact. The zero point costs no instruction per code, it enters once per group with the
+// group's activation sum. The two groups' MMA chains run side by side.
+__device__ __forceinline__ void moe_products(float (&acc)[4], const MoeItem& m, const MoeFrag& f) {
+  float tq[2][4];
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk) {
-    uint4 w[N][2];
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) w[i][g] = *reinterpret_cast<const uint4*>(code[i] + g * 1024 + kk * 512);
+  for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
     for (int s4 = 0; s4 < 4; ++s4)
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+      for (int g = 0; g < 2; ++g) {
+        const uint4& wv = m.w[g][kk];
+        const uint32_t q = (s4 == 0) ? wv.x : (s4 == 1) ? wv.y : (s4 == 2) ? wv.z : wv.w;
+        const uint32_t q8 = q >> 8;
+        const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
+        const uint4& xq = f.v[g][kk][s4 >> 1];
+        const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
+        if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[g], a, b0, b1);
+        else mma_m16n8k16_f32(tq[g], a, b0, b1);
+      }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t q = (s4 == 0) ? w[i][g].x : (s4 == 1) ? w[i][g].y : (s4 == 2) ? w[i][g].z : w[i][g].w;
-          const uint32_t q8 = q >> 8;
-          const uint32_t a[4] = {q & 0x000F000Fu, q & 0x00F000F0u, q8 & 0x000F000Fu, q8 & 0x00F000F0u};
-          const uint4& xq = f.v[g][kk][s4 >> 1];
-          const uint32_t b0 = (s4 & 1) ? xq.z : xq.x, b1 = (s4 & 1) ? xq.w : xq.y;
-          if (kk == 0 && s4 == 0) mma_m16n8k16_f32_zero(tq[i][g], a, b0, b1);
-          else mma_m16n8k16_f32(tq[i][g], a, b0, b1);
-        }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-      moe_scale(acc[i], tq[i][g], f.s[g], *reinterpret_cast<const uint32_t*>(scale[i] + g * 32), zero[i][g * 8]);
+  for (int g = 0; g < 2; ++g) moe_scale(acc, tq[g], f.s[g], m.s[g], m.z[g]);
 }
 
 __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a) {
   constexpr int S = kMoeStages;
   extern __shared__ __align__(128) uint8_t smem[];
   float* rec = reinterpret_cast<float*>(smem + S * kMoeStage);
-  // what a stage or a record holds: block, first unit, units (0: the phase ends), chunk
+  // what a stage or a record holds: block, first unit, units (0: the phase ends), chunk of K
   int4* stage_of = reinterpret_cast<int4*>(rec + kMoeBufs * kMoeCW * 2 * kMoeRec);
   int4* event_of = stage_of + S;
   uint64_t* full = reinterpret_cast<uint64_t*>(event_of + kMoeBufs);
@@ -346,7 +342,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     else if (a.E * ((a.T + 1) / 2) <= nc) logits(std::integral_constant<int, 2>{});
     else if (a.E * ((a.T + 3) / 4) <= nc) logits(std::integral_constant<int, 4>{});
     else logits(std::integral_constant<int, 8>{});
-    __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) moe_await(moe_arrive(), s_abort, budget);
     __syncthreads();
@@ -419,20 +414,23 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     auto produce = [&](bool second) -> bool {
       const MoeCut& k = second ? k2 : k1;
       const uint8_t *q = second ? a.dn_q : a.gu_q, *sc = second ? a.dn_s : a.gu_s, *z = second ? a.dn_z : a.gu_z;
-      const size_t pairs = second ? a.dn_pairs : a.gu_pairs, total = a.E * pairs;
+      const size_t pairs = second ? a.dn_pairs : a.gu_pairs;
       const int P = second ? a.K / 32 : a.I / 16;
-      auto stage = [&](int4 what, int half) -> bool {          // `what.z` units' tiles of one half
+      auto stage = [&](int4 what) -> bool {
         if (!moe_wait(&empty[slot], phase ^ 1, hint, s_abort, budget)) return false;
         uint8_t* sb = smem + slot * kMoeStage;
-        const int p0 = what.w * k.len, n = what.z * min(k.len, k.Q - p0);
+        const int p0 = what.w * k.len, n = what.z * min(k.len, k.Q - p0);      // items of a half
         stage_of[slot] = what;
-        mbar_arrive_expect_tx(&full[slot], n * kItem);
+        mbar_arrive_expect_tx(&full[slot], 2 * n * kItem);
         if (n > 0) {
-          const size_t tp = static_cast<size_t>(l_expert[what.x]) * pairs + static_cast<size_t>(half * P + what.y) * k.Q + p0;
-          if (AWQ_CHECK(n <= kMoeStageItems && tp + n <= total)) {
-            bulk_g2s(sb, q + tp * kPairCodeBytes, n * kPairCodeBytes, &full[slot]);
-            bulk_g2s(sb + kMoeOffS, sc + tp * kPairScaleBytes, n * kPairScaleBytes, &full[slot]);
-            bulk_g2s(sb + kMoeOffZ, z + tp * kPairZeroBytes, n * kPairZeroBytes, &full[slot]);
+          size_t tp = static_cast<size_t>(l_expert[what.x]) * pairs + static_cast<size_t>(what.y) * k.Q + p0;
+          for (int h = 0; h < 2; ++h) {
+            if (AWQ_CHECK(n <= kMoeTile && tp + n <= a.E * pairs)) {
+              bulk_g2s(sb + h * kMoeTile * kPairCodeBytes, q + tp * kPairCodeBytes, n * kPairCodeBytes, &full[slot]);
+              bulk_g2s(sb + kMoeOffS + h * kMoeTile * kPairScaleBytes, sc + tp * kPairScaleBytes, n * kPairScaleBytes, &full[slot]);
+              bulk_g2s(sb + kMoeOffZ + h * kMoeTile * kPairZeroBytes, z + tp * kPairZeroBytes, n * kPairZeroBytes, &full[slot]);
+            }
+            tp += static_cast<size_t>(P) * k.Q;
           }
         }
         ++issued;
@@ -444,7 +442,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
           const int v = u / P, j = u - v * P;
           const int x = second ? v / k.chunks : v, n = min(k.strips, min(P - j, end - u));
           for (int c = second ? v - x * k.chunks : 0;; ++c) {
-            if (!stage(make_int4(x, j, n, c), 0) || !stage(make_int4(x, j, n, c), 1)) return false;
+            if (!stage(make_int4(x, j, n, c))) return false;
             if (second || c + 1 == k.chunks) break;
           }
           u += n;
@@ -463,7 +461,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         if (u >= all) break;
         if (!units(static_cast<int>(u), static_cast<int>(min(u + k.strips, static_cast<long long>(all))))) return false;
       }
-      return stage(make_int4(0, 0, 0, 0), 0);  // the phase ends
+      return stage(make_int4(0, 0, 0, 0));     // the phase ends
     };
     if (produce(false)) produce(true);
     // drain: every copy this thread issued has landed before the CTA may exit
@@ -478,9 +476,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
     // the sum of the records of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24,
     // row r + 8: 2^-20)
     auto sum = [&](int half, int w0, int nw, int col, int row) {
+      const float* p = rec_of(w0, half) + col * 20 + row;
       float v = 0.0f;
-#pragma unroll 8
-      for (int w = 0; w < nw; ++w) v += rec_of(w0 + w, half)[col * 20 + row];
+      if (nw == kMoeCW) {
+#pragma unroll
+        for (int w = 0; w < kMoeCW; ++w) v += p[w * 2 * kMoeRec];
+      } else {
+        for (int w = 0; w < nw; ++w) v += p[w * 2 * kMoeRec];
+      }
       return v * (row < 8 ? 16777216.0f : 1048576.0f);
     };
     const int lane0 = 32 * (warp - kMoeCW - 1) + lane;
@@ -494,10 +497,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         if (nu > 0) {
           const int first = l_first[x], cnt = l_first[x + 1] - first;
           if (ph == 0) {
-            for (int q = lane0; q < 16 * nu * cnt; q += 32 * kMoeEpi) {
-              const int row = q & 15, i = (q >> 4) % nu, col = (q >> 4) / nu;
+            for (int q = lane0; q < (16 * cnt) << k1.shift; q += 32 * kMoeEpi) {
+              const int row = q & 15, i = (q >> 4) & (k1.strips - 1), col = q >> (4 + k1.shift);
               const int i_row = 16 * (what.y + i) + row;
-              if (!AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
+              if (i >= nu || !AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
               const float g = sum(0, i * k1.wide, k1.len, col, row), v = sum(1, i * k1.wide, k1.len, col, row);
               float hv = silu_mul(g, v) * l_p[first + col];
               if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
@@ -505,10 +508,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
             }
           } else {
             const int nw = min(k2.len, k2.Q - what.w * k2.len);
-            for (int q = lane0; q < 32 * nu * cnt; q += 32 * kMoeEpi) {
-              const int row = q & 15, i = (q >> 4) % nu, half = (q >> 4) / nu & 1, col = (q >> 5) / nu;
+            for (int q = lane0; q < (32 * cnt) << k2.shift; q += 32 * kMoeEpi) {
+              const int row = q & 15, i = (q >> 4) & (k2.strips - 1), half = (q >> (4 + k2.shift)) & 1, col = q >> (5 + k2.shift);
               const int k = 16 * (half * (a.K / 32) + what.y + i) + row;
-              if (!AWQ_CHECK(first + col < n_assign && k < a.K)) continue;
+              if (i >= nu || !AWQ_CHECK(first + col < n_assign && k < a.K)) continue;
               a.part[(static_cast<size_t>(first + col) * k2.chunks + what.w) * a.K + k] = sum(half, i * k2.wide, nw, col, row);
             }
           }
@@ -518,8 +521,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         next_event();
         if (nu == 0) break;
       }
-      // the grid-wide barrier: every CTA's results are written (release) and visible (acquire)
-      __threadfence();
+      // the grid-wide barrier: every CTA's results are written and visible
       __syncwarp();
       if (lane == 0) mbar_arrive(edone);
       if (warp == kMoeCW + 1) {
@@ -536,13 +538,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 
   // ------------------------------------------------------------------ consumer warps
   const int r = lane >> 2, t = lane & 3;
-  auto release = [&](int n) {
-    __syncwarp();
-    for (int i = 0; i < n; ++i) {
-      if (lane == 0) mbar_arrive(&empty[slot]);
-      advance();
-    }
-  };
   // The fragments of pair `pr` for a block's tokens, and their sums; `row` is the lane's token.
   auto load_frag = [&](MoeFrag& f, const __half* row, int pr, int G) {
 #pragma unroll
@@ -569,58 +564,68 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       f.s[g][1] = d[1];
     }
   };
+  float* const rec0 = rec + warp * 2 * kMoeRec + 2 * t * 20 + r;               // this lane's place in a record
+  const uint8_t* const item0 = smem + lane * 16;
   bool ok = true;
   for (int ph = 0; ph < 2; ++ph) {
-    const MoeCut& k = ph ? k2 : k1;
     const int G = (ph ? a.I : a.K) / kGroup;
-    const int pl = warp % k.wide, sub = warp / k.wide;
+    const int Q = ph ? k2.Q : k1.Q, len = ph ? k2.len : k1.len, wide = ph ? k2.wide : k1.wide;
+    const int last = ph ? 0 : k1.chunks - 1;   // the chunk that completes a unit (phase 2: any)
+    const int pl = warp % wide, sub = warp / wide;
+    const int item = sub * Q + pl;             // of a stage with several strips, one after another
+    const int oc = item * kPairCodeBytes, os = kMoeOffS + item * kPairScaleBytes + (r - 4 * lane) * 4,
+              oz = kMoeOffZ + item * kPairZeroBytes + r - 16 * lane;           // from item0
     float acc[2][4] = {};                      // the unit's two tiles
     MoeFrag f;
     int fx = -1, fc = 0;                       // block and chunk of the fragments
-    while (ok) {
+    bool mine = false;                         // whether the warp has a pair of the chunk
+    while (true) {
       ok = warp_wait(&full[slot], phase);
       if (!ok) break;
       const int4 what = stage_of[slot];
-      const int x = what.x, c = what.w;
       if (what.z > 0) {
-        const int pr = c * k.len + pl;
-        const bool mine = pl < k.len && pr < k.Q;
-        if (x != fx || c != fc) {
-          fx = x;
-          fc = c;
+        if (what.x != fx || what.w != fc) {
+          fx = what.x;
+          fc = what.w;
+          const int pr = fc * len + pl;
+          mine = pl < len && pr < Q;
           // columns past the block's last token repeat it; they are never used
-          const int first = l_first[x], s = first + min(r, l_first[x + 1] - first - 1);
+          const int first = l_first[fx], s = first + min(r, l_first[fx + 1] - first - 1);
           const __half* row = ph ? a.h + static_cast<size_t>(s) * a.I : a.x + static_cast<size_t>(l_token[s]) * a.K;
           if (mine) load_frag(f, row, pr, G);
         }
-        const int next = slot + 1 == S ? 0 : slot + 1;         // the other half's stage
-        ok = warp_wait(&full[next], next == 0 ? phase ^ 1 : phase);
-        if (!ok) break;
         if (mine && sub < what.z) {
-          const int item = sub * k.Q + pl;     // several strips: one after another
-          const uint8_t *s0 = smem + slot * kMoeStage, *s1 = smem + next * kMoeStage;
-          const int oc = item * kPairCodeBytes + lane * 16, os = kMoeOffS + item * kPairScaleBytes + r * 4,
-                    oz = kMoeOffZ + item * kPairZeroBytes + r;
-          const uint8_t* const code[2] = {s0 + oc, s1 + oc};
-          const uint8_t* const scale[2] = {s0 + os, s1 + os};
-          const uint8_t* const zero[2] = {s0 + oz, s1 + oz};
-          moe_pairs<2>(acc, code, scale, zero, f);
+          const uint8_t* sb = item0 + slot * kMoeStage;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            MoeItem m;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              m.w[g][0] = *reinterpret_cast<const uint4*>(sb + oc + h * kMoeTile * kPairCodeBytes + g * 1024);
+              m.w[g][1] = *reinterpret_cast<const uint4*>(sb + oc + h * kMoeTile * kPairCodeBytes + g * 1024 + 512);
+              m.s[g] = *reinterpret_cast<const uint32_t*>(sb + os + h * kMoeTile * kPairScaleBytes + g * 32);
+              m.z[g] = sb[oz + h * kMoeTile * kPairZeroBytes + g * 8];
+            }
+            moe_products(acc[h], m, f);
+          }
         }
       }
-      release(what.z > 0 ? 2 : 1);
-      if (ph == 0 && what.z > 0 && c + 1 < k.chunks) continue;   // the unit's sums go on
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      advance();
+      if (what.z > 0 && ph == 0 && what.w != last) continue;   // the unit's sums go on
       ok = warp_wait(&rempty[rbuf], rphase ^ 1);
       if (!ok) break;
+      float* p = rec0 + rbuf * (kMoeCW * 2 * kMoeRec);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float* p = rec_of(warp, h) + 2 * t * 20 + r;
-        p[0] = acc[h][0];
-        p[20] = acc[h][1];
-        p[8] = acc[h][2];
-        p[28] = acc[h][3];
+        p[h * kMoeRec] = acc[h][0];
+        p[h * kMoeRec + 20] = acc[h][1];
+        p[h * kMoeRec + 8] = acc[h][2];
+        p[h * kMoeRec + 28] = acc[h][3];
         acc[h][0] = acc[h][1] = acc[h][2] = acc[h][3] = 0.0f;
       }
-      if (warp == 0 && lane == 0) event_of[rbuf] = what;
+      if (threadIdx.x == 0) event_of[rbuf] = what;
       __syncwarp();
       if (lane == 0) mbar_arrive(&rfull[rbuf]);
       next_event();
@@ -631,18 +636,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 
   // ---- phase 3: y, four values a thread; a token's partial sums in the order of its choices and of K
   if (!ok) return;
-  const int quads = a.K / 4;
-  for (int q = c0 * 32 * kMoeCW + threadIdx.x; q < a.T * quads; q += nc * 32 * kMoeCW) {
+  const int quads = a.K / 4, terms = a.top * k2.chunks;
+  for (int q = threadIdx.x * nc + c0; q < a.T * quads; q += nc * 32 * kMoeCW) {
     const int tok = q / quads, k4 = (q - tok * quads) * 4;
+    const int* of = l_of + tok * a.top;
     float v[4] = {};
-    for (int i = 0; i < a.top; ++i) {
-      const float* p = a.part + static_cast<size_t>(l_of[tok * a.top + i]) * k2.chunks * a.K + k4;
-      for (int c = 0; c < k2.chunks; ++c) {
-        const uint4 w = ld_coherent_v4(p + static_cast<size_t>(c) * a.K);
-        v[0] += __uint_as_float(w.x);
-        v[1] += __uint_as_float(w.y);
-        v[2] += __uint_as_float(w.z);
-        v[3] += __uint_as_float(w.w);
+    for (int n = 0; n < terms; n += 4) {       // four loads under way
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = min(n + j, terms - 1) / k2.chunks, c = min(n + j, terms - 1) - i * k2.chunks;
+        w[j] = ld_coherent_v4(a.part + (static_cast<size_t>(of[i]) * k2.chunks + c) * a.K + k4);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (n + j >= terms) break;
+        v[0] += __uint_as_float(w[j].x);
+        v[1] += __uint_as_float(w[j].y);
+        v[2] += __uint_as_float(w[j].z);
+        v[3] += __uint_as_float(w[j].w);
       }
     }
     const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
