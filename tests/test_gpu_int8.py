@@ -179,3 +179,61 @@ def test_weights_quantized_right_before_the_product():
         ys.append(P.awq_w8a8_linear(xqd, sxd, *out))
     for W, y in zip(Ws, ys):
         check_y(y, B.w8a8(xq, sx, *B.quantize_rows(W)))
+
+
+def test_outputs_and_codes_past_2_31_elements():
+    torch, P = torch_mod(), lib()
+    M, N, K = 65600, 32768, 48
+    rng = np.random.default_rng(9)
+    wq = rng.integers(-127, 128, (N, K)).astype(np.int8)
+    sw = rng.uniform(0.5, 2, N).astype(np.float32) * 1e-3
+    x = torch.randn((M, K), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).half()
+    y = P.awq_w8a8_forward(x, dev(wq), dev(sw))
+    assert y.numel() > 2 ** 31
+    rows = [0, 1, 777, 65535, 65536, M - 1]
+    xq, sx = B.quantize_rows(host(x[rows]))
+    check_y(y[rows], B.w8a8(xq, sx, wq, sw))
+    del y
+    W = torch.zeros((M, N), dtype=torch.float16, device="cuda")
+    tail = rng.standard_normal((3, N)).astype(np.float16)
+    W[-3:] = dev(tail)
+    q, step = P.awq_quantize_channels(W)
+    qr, sr = B.quantize_rows(tail)
+    same_bits(host(step[-3:]), sr)
+    same_bits(host(q[-3:]), qr)
+    assert not step[:-3].any() and not q[:-3].any()
+
+
+def test_refusals_on_the_device():
+    torch, P = torch_mod(), lib()
+    layer = P.AWQInt8Linear.from_float(torch.zeros((32, 64), dtype=torch.float16, device="cuda"))
+    x = torch.zeros((4, 64), dtype=torch.float16, device="cuda")
+    assert layer(x).shape == (4, 32) and P.awq_w8a8_forward(x, layer.wq, layer.sw).shape == (4, 32)
+    for bad, error in ((x.t().contiguous().t(), ValueError), (x[:, :32], ValueError), (x[:0], ValueError), (x.float(), TypeError),
+                       (x.cpu(), ValueError), (x[0], ValueError), (x.cpu().numpy(), TypeError)):
+        with pytest.raises(error):
+            layer(bad)
+    with pytest.raises(ValueError, match="workspace"):
+        layer(x, workspace=torch.empty(16, dtype=torch.int8, device="cuda"))
+    with pytest.raises(ValueError, match="shape"):
+        layer(x, y=torch.empty((4, 31), dtype=torch.float16, device="cuda"))
+
+
+def test_two_streams_at_once():
+    torch, P = torch_mod(), lib()
+    rng = np.random.default_rng(21)
+    work = []
+    for M, N, K in ((1, 4096, 2048), (300, 1000, 528)):
+        W, x = (rng.standard_normal((n, K)).astype(np.float16) for n in (N, M))
+        work.append((P.AWQInt8Linear.from_float(dev(W)), dev(x), torch.cuda.Stream(), B.w8a8(*B.quantize_rows(x), *B.quantize_rows(W))))
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(20):
+        for layer, x, s, ref in work:
+            with torch.cuda.stream(s):
+                out.append((layer(x), ref))
+    torch.cuda.synchronize()
+    for y, ref in out[-4:]:
+        check_y(y, ref)
+    assert all(torch.equal(a[0], b[0]) for a, b in zip(out[::2], out[2::2]))
+    assert P.awq_poll_device_status() == P.AWQ_OK

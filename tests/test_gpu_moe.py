@@ -269,3 +269,50 @@ def test_wait_budget_runs_out_then_recovers():
     ref = B.w8a8(xq, np.full(600, 1e-3, np.float32), wq, np.full(2048, 1e-3, np.float32))
     y = host(P.awq_w8a8_linear(xd, ones(600), wd, ones(2048)))
     assert (np.abs(y - ref) <= (2.0 ** -11 + 2.0 ** -22) * np.abs(ref) + 2.0 ** -25).all()
+
+
+def test_experts_past_32_bit_offsets():
+    """512 experts whose packed gate/up layers take more than 4 GB: the first and the last are reached."""
+    torch, P = torch_mod(), lib()
+    E, K, I = 512, 2048, 4224
+    rng = np.random.default_rng(3)
+    stacks = []
+    for N, Kin in ((2 * I, K), (K, I)):
+        qb, sb, zb = P._packed_sizes_host(N, Kin)
+        stacks.append((torch.zeros((E, qb // 4), dtype=torch.int32, device="cuda"),
+                       torch.zeros((E, sb // 2), dtype=torch.float16, device="cuda"),
+                       torch.zeros((E, zb), dtype=torch.uint8, device="cuda")))
+    assert stacks[0][0][: E - 1].numel() * 4 > 2 ** 32
+    gu_w, dn_w = {}, {}
+    for e in (0, E - 1):
+        for stack, (N, Kin), keep in ((stacks[0], (2 * I, K), gu_w), (stacks[1], (K, I), dn_w)):
+            q, S, z = O.quantize_groups((rng.standard_normal((N, Kin)) * 0.03).astype(np.float16))
+            for t, v in zip(stack, O.pack(q, S, z)):
+                t[e] = dev(v.view(np.int32) if v.dtype == np.uint32 else v)
+            keep[e] = O.dequantize(q, S, z).astype(np.float64)
+    x = np.abs(rng.standard_normal((2, K))).astype(np.float16)
+    x[1] = -x[1]
+    router = np.zeros((E, K), np.float16)
+    router[0], router[E - 1] = 0.01, -0.01          # token 0 chooses the first, token 1 the last
+    y = P.awq_moe_w4a16(dev(x), dev(router), stacks[0], stacks[1], I, 1)
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    for t, e in ((0, 0), (1, E - 1)):
+        ref, bound, _ = B.moe(x[t:t + 1], router[[e]], gu_w[e][None], dn_w[e][None], 1, True)
+        assert (np.abs(host(y)[t] - ref[0]) <= bound[0]).all()
+
+
+def test_refusals_on_the_device():
+    torch, P = torch_mod(), lib()
+    c = Case(4, 8, 2, 256, 128)
+    layer = c.layer()
+    x = dev(c.x)
+    with pytest.raises(ValueError, match="contiguous"):
+        layer(torch.zeros((256, 4), dtype=torch.float16, device="cuda").t())
+    with pytest.raises(TypeError, match="float16"):
+        layer(x.float())
+    with pytest.raises(ValueError, match="tokens"):
+        layer(torch.zeros((33, 256), dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError, match="workspace"):
+        layer(x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="CUDA"):
+        layer(x.cpu())

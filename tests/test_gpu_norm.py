@@ -133,3 +133,32 @@ def test_captured_chain_into_a_quantized_layer():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, block()))
+
+
+def test_rows_past_2_31_elements():
+    torch, P = torch_mod(), lib()
+    K, M = 32768, 65540
+    y = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    r = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    assert y.numel() > 2 ** 31
+    a = inputs(3, K, True, 0, True)
+    y[-3:], r[-3:] = dev(a["y"]), dev(a["residual"])
+    d = to_dev(a)
+    h, x = P.awq_residual_norm(y, r, d["weight"], post_weight=d["post_weight"], s=d["s"])
+    check((h[-3:], x[-3:]), a, "last rows")
+    assert not h[:-3].any() and not x[:-3].any()
+
+
+def test_refusals_on_the_device():
+    torch, P = torch_mod(), lib()
+    y = torch.zeros((4, 64), dtype=torch.float16, device="cuda")
+    w = torch.ones(64, dtype=torch.float16, device="cuda")
+    P.awq_residual_norm(y, y, w)
+    for args, kw, error in (((y.t(), None, w), {}, ValueError), ((y, y[:2], w), {}, ValueError), ((y, y, w[:32]), {}, ValueError),
+                            ((y.float(), None, w), {}, TypeError), ((y, y.cpu(), w), {}, ValueError),
+                            ((y[:, :12].contiguous(), None, w[:12]), {}, ValueError), ((y, y, w), dict(gate=w), ValueError),
+                            ((y, y, w), dict(eps=-1.0), ValueError), ((y, y, w), dict(alpha=float("inf")), ValueError),
+                            ((y, y, w), dict(s=w), TypeError), ((y, y, w), dict(out=(None, None)), ValueError),
+                            ((None, y, w), {}, TypeError), ((y, y, None), {}, TypeError)):
+        with pytest.raises(error):
+            P.awq_residual_norm(*args, **kw)

@@ -175,6 +175,12 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _fits(t, dtype, shape, device: int) -> bool:
+    """Whether t is a contiguous tensor of this type and shape on the given (current) device: what the
+    validators check, without their messages. The calls that are made once per token ask this first."""
+    return type(t) is _torch_mod.Tensor and t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
 def _need(t, dtype, name, dims=None, require_cuda=True):
     torch = _torch_mod or _torch()
     if (type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous() and (dims is None or t.dim() == dims) and
@@ -627,6 +633,12 @@ class AWQInt8Linear:
         return cls(wq, sw, s)
 
     def __call__(self, x, y=None, workspace=None):
+        # the weights were checked when the layer was made; they and x have to be on the current device
+        torch = _torch()
+        dev = torch.cuda.current_device()
+        if (y is None and type(x) is torch.Tensor and x.dim() == 2 and x.shape[0] > 0 and self.wq.get_device() == dev and
+                _fits(x, torch.float16, (x.shape[0], self.K), dev)):
+            return _w8a8_forward(x, self.wq, self.sw, self.s, None, workspace)
         return awq_w8a8_forward(x, self.wq, self.sw, self.s, y, workspace)
 
 
@@ -652,6 +664,10 @@ def validate_w8a8_forward(x, wq, sw, s, y, require_cuda=True):
 def awq_w8a8_forward(x, wq, sw, s=None, y=None, workspace=None):
     """A whole 8-bit linear layer: awq_quantize_tokens(x, s), then awq_w8a8_linear, in one call."""
     validate_w8a8_forward(x, wq, sw, s, y)
+    return _w8a8_forward(x, wq, sw, s, y, workspace)
+
+
+def _w8a8_forward(x, wq, sw, s, y, workspace):
     (M, K), N = x.shape, wq.shape[0]
     lib = load_library()
     need = (M * K + 255) // 256 * 256 + 4 * M        # awq_w8a8_workspace_bytes(M, K)
@@ -719,12 +735,18 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
         if x is None:
             raise ValueError("x is always written")
     alpha, eps = float(alpha), float(eps)
-    validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
+    dev, f16 = torch.cuda.current_device(), torch.float16
+    shape = y.shape if type(y) is torch.Tensor else ()
+    if not (out is None and gate is None and post_weight is None and len(shape) == 2 and _fits(y, f16, shape, dev) and
+            0 < shape[0] and 8 <= shape[1] <= NORM_MAX_K and shape[1] % 8 == 0 and
+            (residual is None or _fits(residual, f16, shape, dev)) and _fits(weight, f16, shape[1:], dev) and
+            (s is None or _fits(s, torch.float32, shape[1:], dev)) and -3.0e38 <= alpha <= 3.0e38 and 0.0 <= eps <= 3.0e38):
+        validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
     if out is None:
         x = torch.empty_like(y)
         if want_h:
             h = torch.empty_like(y)
-    M, K = y.shape
+    M, K = shape
     per = M // gate.shape[0] if gate is not None else 1
     st = load_library().awq_residual_norm(y.data_ptr(), _ptr(residual), _ptr(gate), per, _ptr(post_weight),
                                           weight.data_ptr(), _ptr(s), alpha, eps, M, K, _ptr(h), x.data_ptr(),
