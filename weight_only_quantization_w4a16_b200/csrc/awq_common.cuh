@@ -185,6 +185,42 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// A bounded wait whose common case, the phase complete at the first look or within one suspension, stays
+// small in the instruction stream. hint_ns comes from brief_hint; 0 stands for a short budget, which is
+// polled without suspension: a suspended wait outlasts it.
+__device__ __forceinline__ uint32_t brief_hint(unsigned long long budget_ns) {
+  return budget_ns < kShortBudgetNs ? 0u : 1000000u;
+}
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool mbar_wait_longer(uint64_t* bar, uint32_t parity, uint32_t hint_ns, volatile int* abort,
+                                                     unsigned long long budget_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!(hint_ns == 0 ? mbar_test_wait(bar, parity) : mbar_try_wait_for(bar, parity, hint_ns))) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > budget_ns) {
+      *abort = 1;
+      atomicOr(&g_dev_status, kDevStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool mbar_wait_brief(uint64_t* bar, uint32_t parity, uint32_t hint_ns, volatile int* abort,
+                                                unsigned long long budget_ns) {
+  return (hint_ns != 0 && mbar_try_wait_for(bar, parity, hint_ns)) ||
+         mbar_wait_longer(bar, parity, hint_ns, abort, budget_ns);
+}
+
 // ---------------------------------------------------------------------------
 // Thread-block clusters: the cluster barrier, split into arrive and wait (all 32 lanes of a warp
 // execute each together), and shared-memory access to the other CTAs of the cluster.

@@ -154,14 +154,22 @@ __global__ void __launch_bounds__(1024) awq_quantize_rows_kernel(const __half* _
 // ---------------------------------------------------------------------------- int8 product
 // The weights are the MMA's A operand (rows = output channels), the tokens its B operand (columns),
 // so one kernel serves one token (BT = 16 columns) and a long prompt (BT = 256). Per CTA:
-//   warp 0 (one lane): producer — per 128-byte k block one TMA box of the tile's weight rows and one of
-//       BT token rows (128-byte swizzle, zero fill past M, N and K) into a ring; the first ring
-//       pass of weights is requested before the wait on the stream's predecessor;
-//   warp 1 (one lane): tcgen05.mma kind::i8, 128 x BT x 32 per instruction, int32 in tensor memory;
+//   warp 0: producer — per 128-byte k block one TMA box of the tile's weight rows and one of BT token rows
+//       (128-byte swizzle, zero fill past M, N and K) into a ring; the first ring pass of weights is
+//       requested before the wait on the stream's predecessor;
+//   warp 1: tcgen05.mma kind::i8, 128 x BT x 32 per instruction, int32 in tensor memory;
 //   warps 2..: epilogue — tcgen05.ld, scales in fp32, fp16 stores, the channels of a warp side by side.
 // A tile has 128 MT weight rows. ks > 1: the CTAs of a cluster split a tile's k blocks, and each adds
 // the int32 partial sums (exact in any order) of its share of the token columns from distributed
 // shared memory.
+//
+// Bound: up to 64 tokens by the weight bytes, long prompts by the tensor pipe (128 cycles per MMA at BT = 256) and, run without a pause, by the power
+// limit. In between the two issuing warps bound it: a wait, four MMAs and a commit took 728 cycles per k
+// block, whatever BT, while a single lane ran them; with a converged warp, elect.sync, a wait without the
+// deadline code inside and descriptors in 32 bits they take 530, and 390 per block when two blocks share a
+// stage. A second producer warp for the tokens was slower: its barrier is one more wait for the MMA warp.
+// Rows that do not start on 128-byte lines (K % 128 != 0) cost the copies two lines per row: 3 cycles
+// per row and k block, which bounds 333 x 5001 x 4112.
 struct Int8Args {
   const float* sx;
   const float* sw;
@@ -231,6 +239,23 @@ __device__ __forceinline__ __half i8_out(int sum, float sx, float sw) {
   return __float2half_rn(static_cast<float>(sum) * (sx * sw));
 }
 
+// One lane of the converged warp. (Code behind elect.sync is known to have one thread, which the copy and
+// MMA instructions need.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void mbar_expect_tx_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_at(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 template <int BT, int MT>
 __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
     awq_w8a8_kernel(const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_x,
@@ -251,7 +276,8 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + kI8Bars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that a warp's index is the same in all of its lanes)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int ks = a.ks;
   const int rank = ks > 1 ? static_cast<int>(blockIdx.x) % ks : 0;
   const int KB = (a.K + 127) / 128;
@@ -298,84 +324,99 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
   const uint32_t tmem_base = *s_tmem;
   const unsigned long long budget = g_wait_budget_ns;
 
+  const uint32_t base = smem_u32(smem), full0 = smem_u32(full);
+  const uint32_t hint = brief_hint(budget);
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_brief(bar, parity, hint, s_abort, budget));
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      auto issue_w = [&](int slot, int rb, int kb, int n) {
-        uint8_t* sb = smem + slot * stage_bytes;
-        mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(n * (a_bytes + b_bytes)));
-        for (int j = 0; j < n; ++j) tma_load_2d(sb + j * a_bytes, &tmap_w, (kb + j) * 128, rb * kRows, &full[slot]);
-      };
-      auto issue_x = [&](int slot, int tt, int kb, int n) {
-        uint8_t* sb = smem + slot * stage_bytes + kpb * a_bytes;
-        for (int j = 0; j < n; ++j) tma_load_2d(sb + j * b_bytes, &tmap_x, (kb + j) * 128, tt * BT, &full[slot]);
-      };
-      int rb, tt;
-      // first ring pass of the first tile's weights before the wait on the predecessor
-      int pre = 0;
-      if (tile0 < ntiles) {
-        tile_at(tile0, rb, tt);
-        for (int kb = kb0; kb < kb1 && pre < S; kb += kpb, ++pre) issue_w(pre, rb, kb, min(kpb, kb1 - kb));
-      }
-      pdl_wait();
-      int slot = 0, n_issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = tile0; ok && t < ntiles; t += step) {
-        tile_at(t, rb, tt);
-        for (int kb = kb0; kb < kb1; kb += kpb) {
-          const int n = min(kpb, kb1 - kb);
-          if (n_issued >= pre) {
-            if (!mbar_wait_bounded(&empty[slot], phase ^ 1, s_abort, budget)) { ok = false; break; }
-            issue_w(slot, rb, kb, n);
-          }
-          issue_x(slot, tt, kb, n);
-          ++n_issued;
-          if (++slot == S) { slot = 0; phase ^= 1; }
+    auto issue_w = [&](int slot, int row, int kb, int n) {
+      const uint32_t dst = base + slot * stage_bytes, bar = full0 + 8 * slot;
+      mbar_expect_tx_at(bar, static_cast<uint32_t>(n * (a_bytes + b_bytes)));
+      for (int j = 0; j < n; ++j) tma_load_2d_at(dst + j * a_bytes, &tmap_w, (kb + j) * 128, row, bar);
+    };
+    auto issue_x = [&](int slot, int row, int kb, int n) {
+      const uint32_t dst = base + slot * stage_bytes + kpb * a_bytes, bar = full0 + 8 * slot;
+      for (int j = 0; j < n; ++j) tma_load_2d_at(dst + j * b_bytes, &tmap_x, (kb + j) * 128, row, bar);
+    };
+    int rb, tt;
+    // first ring pass of the first tile's weights before the wait on the predecessor
+    int pre = 0;
+    if (tile0 < ntiles) {
+      tile_at(tile0, rb, tt);
+      for (int kb = kb0; kb < kb1 && pre < S; kb += kpb, ++pre)
+        if (elect_one()) issue_w(pre, rb * kRows, kb, min(kpb, kb1 - kb));
+    }
+    __syncwarp();
+    pdl_wait();
+    int slot = 0, n_issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = tile0; ok && t < ntiles; t += step) {
+      tile_at(t, rb, tt);
+      for (int kb = kb0; kb < kb1; kb += kpb) {
+        const int n = min(kpb, kb1 - kb);
+        if (n_issued >= pre && !warp_wait(&empty[slot], phase ^ 1)) { ok = false; break; }
+        if (elect_one()) {
+          if (n_issued >= pre) issue_w(slot, rb * kRows, kb, n);
+          issue_x(slot, tt * BT, kb, n);
         }
+        __syncwarp();
+        ++n_issued;
+        if (++slot == S) { slot = 0; phase ^= 1; }
       }
-      // drain: every copy this thread issued has landed before the CTA may exit
-      int never = 0;
+    }
+    // drain: every copy this warp issued has landed before the CTA may exit
+    int never = 0;
+    if (lane == 0)
       for (int i = max(0, n_issued - S); i < n_issued; ++i)
         mbar_wait_bounded(&full[i % S], static_cast<uint32_t>((i / S) & 1), &never, kDrainBudgetNs);
-    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_s8_s32(128, BT);
-      int slot = 0, it = 0;
-      uint32_t phase = 0;
-      bool ok = true, any = false;
-      for (int t = tile0; ok && t < ntiles; t += step, ++it) {
-        const int b = it % C::kNAcc;
-        if (!mbar_wait_bounded(&accempty[b], ((it / C::kNAcc) & 1) ^ 1, s_abort, budget)) { ok = false; break; }
+    constexpr uint32_t idesc = idesc_s8_s32(128, BT);
+    const uint64_t desc_hi = smem_desc_sw128(0) & ~0xFFFFFFFFull;
+    const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_sw128(base));
+    int slot = 0, it = 0;
+    uint32_t phase = 0;
+    bool ok = true, any = false;
+    for (int t = tile0; ok && t < ntiles; t += step, ++it) {
+      const int b = it % C::kNAcc;
+      ok = warp_wait(&accempty[b], ((it / C::kNAcc) & 1) ^ 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::kAcc);
+      for (int kb = kb0; kb < kb1; kb += kpb) {
+        ok = warp_wait(&full[slot], phase);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(b * C::kAcc);
-        for (int kb = kb0; kb < kb1; kb += kpb) {
-          if (!mbar_wait_bounded(&full[slot], phase, s_abort, budget)) { ok = false; break; }
-          tc_fence_after();
-          const int n = min(kpb, kb1 - kb);
-          const uint32_t sa = smem_u32(smem + slot * stage_bytes), sb = sa + kpb * a_bytes;
+        const int n = min(kpb, kb1 - kb);
+        // descriptors count in 16 bytes; shared memory ends well below the 2^18 that their field holds
+        const uint32_t da = desc_lo + ((slot * stage_bytes) >> 4), db = da + ((kpb * a_bytes) >> 4);
+        if (elect_one()) {
           for (int j = 0; j < n; ++j) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
               for (int m = 0; m < MT; ++m)
-                tc_mma_i8(d + m * BT, smem_desc_sw128(sa + j * a_bytes + m * 16384 + 32 * kk),
-                          smem_desc_sw128(sb + j * b_bytes + 32 * kk), idesc, (kb != kb0 || j != 0 || kk != 0) ? 1u : 0u);
+                tc_mma_i8(d + m * BT, desc_hi | (da + ((j * a_bytes + m * 16384 + 32 * kk) >> 4)),
+                          desc_hi | (db + ((j * b_bytes + 32 * kk) >> 4)), idesc, (kb != kb0 || j != 0 || kk != 0) ? 1u : 0u);
           }
-          any = true;
           tc_commit(&empty[slot]);
-          if (++slot == S) { slot = 0; phase ^= 1; }
         }
-        if (!ok) break;
-        tc_commit(&accfull[b]);
+        __syncwarp();
+        any = true;
+        if (++slot == S) { slot = 0; phase ^= 1; }
       }
-      if (any) {
-        int never = 0;
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0, &never, kDrainBudgetNs);
-      }
+      if (ok && elect_one()) tc_commit(&accfull[b]);
+      __syncwarp();
+    }
+    if (any) {
+      int never = 0;
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      if (lane == 0) mbar_wait_bounded(drain, 0, &never, kDrainBudgetNs);
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -399,7 +440,8 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
         __syncwarp();
       }
       const int b = it % C::kNAcc;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&accfull[b], (it / C::kNAcc) & 1, s_abort, budget))) { ok = false; break; }
+      ok = warp_wait(&accfull[b], (it / C::kNAcc) & 1);
+      if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int m = 0; m < MT; ++m) {

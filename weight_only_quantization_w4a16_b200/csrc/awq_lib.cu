@@ -587,13 +587,13 @@ awq_status_t make_i8_map(CUtensorMap* map, const void* q, int rows, int K, int b
 // Token tile, weight rows per tile and K split of the int8 kernel.
 // M <= 64 is bound by the weight bytes, and what counts is how many copies are under way: two CTAs fit
 // an SM (half of its shared memory each), and the form with the most CTAs, up to two per SM, wins;
-// among equals the larger K split with the taller tiles (measured at M = 1: 4096 x 4096 7.3 us with 256
-// CTAs against 9.5 with 128 of 32 rows each; 12288 x 4096 12.4 against 14.6; 28672 x 4096 22.6
-// against 24.1; 4096 x 14336 13.3 against 15.4).
-// Above, a tile takes about `step` cycles per 128-byte k block: L2 delivers some 64 bytes per cycle
-// to an SM, so 256 token columns cost little more than 128 (750, 690 and 560 cycles for 256, 128 and 64,
-// measured). A K split saves rounds of a small grid but pays for the exchange (1500 + 30 per column:
-// 512 x 4096 x 14336 32.5 us with it, 46.9 without), and never pays beyond one round.
+// among equals one without a K split, or else the larger split with the taller tiles (measured at M = 1:
+// 4096 x 14336 12.5 us with 256 CTAs against 17.2 with 64; 28672 x 4096 20.3 unsplit against 21.5;
+// 12288 x 4096 11.3 split four ways against 12.1 two ways).
+// Above, a 128-byte k block takes about `step` cycles: 256 token columns are bound by the tensor pipe, 128
+// and 64 by what the issuing warps do per block (600 and 420 cycles measured; a third more where two CTAs
+// share an SM). A K split saves rounds of a small grid but pays for the exchange (1500 + 30 per column:
+// 512 x 4096 x 14336 30.5 us with it, 44.4 without, at 256 columns), and never pays beyond one round.
 struct Int8Plan {
   int bt, mt, rows, ks;
 };
@@ -605,7 +605,7 @@ Int8Plan int8_plan(int M, int N, int K, int num_sms) {
     for (int mt = 1; mt <= 2; ++mt)
       for (int ks = 1; ks <= 8 && ks <= KB; ks *= 2) {
         const long long ctas = static_cast<long long>(ceil_div(N, 128 * mt)) * ks;
-        if (ctas <= 2 * num_sms && ctas >= most) {
+        if (ctas <= 2 * num_sms && (ctas > most || (ctas == most && best.ks > 1))) {
           most = ctas;
           best.mt = mt;
           best.rows = 128 * mt;
@@ -617,7 +617,7 @@ Int8Plan int8_plan(int M, int N, int K, int num_sms) {
   Int8Plan best = {256, 1, 128, 1};
   double best_cost = 1e300;
   for (int bt = 256; bt >= 64; bt /= 2) {
-    const double step = bt == 256 ? 750.0 : bt == 128 ? 690.0 : 560.0;
+    const double step = bt == 256 ? 600.0 : 420.0;
     const long long tiles = static_cast<long long>(ceil_div(N, 128)) * ceil_div(M, bt);
     const long long slots = bt == 64 ? 2 * num_sms : num_sms;
     for (int ks = 1; ks <= 4 && ks <= KB; ks *= 2) {
@@ -642,7 +642,9 @@ awq_status_t launch_w8a8_cfg(const int8_t* xq, const float* sx, const int8_t* wq
   Int8Args a = {sx, sw, y, M, N, K, ceil_div(N, p.rows), ceil_div(M, BT), p.ks, 0, 0};
   const int KB = ceil_div(K, 128), steps = ceil_div(KB, p.ks);
   const int block = (p.rows + BT) * 128;
-  a.kpb = std::max(1, std::min(std::min(4, steps), 24576 / block));
+  // two k blocks per stage halve the waits and commits of 128 columns (512 x 4096 x 4096 14.3 -> 12.0 us);
+  // 256 columns would have two stages left (344 -> 440 us at 4096 x 28672 x 4096)
+  a.kpb = BT == 128 ? std::min(2, steps) : 1;
   // M <= 64: at most half of an SM's shared memory, so that the next call's CTAs can already be
   // resident and read their first weights while this one's end (a stream of 96 KB per SM is enough)
   constexpr int pad = Int8Cfg<BT, MT>::kSxBytes;

@@ -125,16 +125,6 @@ __device__ __forceinline__ void moe_await(unsigned long long target, volatile in
   }
 }
 
-// A bounded wait whose common case, the phase complete at the first look or within one suspension, stays
-// small in the instruction stream.
-static __device__ __noinline__ bool moe_wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned long long budget) {
-  return mbar_wait_bounded(bar, parity, abort, budget);
-}
-__device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity, uint32_t hint, volatile int* abort,
-                                         unsigned long long budget) {
-  return mbar_try_wait_for(bar, parity, hint) || moe_wait_longer(bar, parity, abort, budget);
-}
-
 __device__ __forceinline__ uint4 ld_coherent_v4(const void* p) {
   uint4 v;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
@@ -390,7 +380,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   // are divided evenly, and the last eighth of many is drawn. The producer leaves word of each stage's
   // content beside it, from which the others learn what to do.
   const MoeCut k1((a.K / kGroup + 1) / 2), k2((a.I / kGroup + 1) / 2);
-  const uint32_t hint = static_cast<uint32_t>(min(budget, 1000000ull));
+  const uint32_t hint = brief_hint(budget);
   int slot = 0;
   uint32_t phase = 0;
   auto advance = [&]() {
@@ -403,7 +393,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   };
   auto rec_of = [&](int w, int half) { return rec + ((rbuf * kMoeCW + w) * 2 + half) * kMoeRec; };
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xFFFFFFFFu, moe_wait(bar, parity, hint, s_abort, budget));
+    return __all_sync(0xFFFFFFFFu, mbar_wait_brief(bar, parity, hint, s_abort, budget));
   };
 
   if (warp == kMoeCW) {
@@ -417,7 +407,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       const size_t pairs = second ? a.dn_pairs : a.gu_pairs;
       const int P = second ? a.K / 32 : a.I / 16;
       auto stage = [&](int4 what) -> bool {
-        if (!moe_wait(&empty[slot], phase ^ 1, hint, s_abort, budget)) return false;
+        if (!mbar_wait_brief(&empty[slot], phase ^ 1, hint, s_abort, budget)) return false;
         uint8_t* sb = smem + slot * kMoeStage;
         const int p0 = what.w * k.len, n = what.z * min(k.len, k.Q - p0);      // items of a half
         stage_of[slot] = what;
