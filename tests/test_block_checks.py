@@ -186,3 +186,10 @@ def test_binding_checks_of_the_experts():
                         (half(3, 256), half(2, 256), "shape")):
         with pytest.raises(ValueError, match=match):
             P._validate_moe_tokens(x, y, 8, 256, require_cuda=False)
+
+
+def test_expert_layer_on_another_device_is_refused():
+    layer = object.__new__(P.AWQMoE)         # a layer whose weights are not on the current device
+    layer.router = half(8, 256)
+    with pytest.raises((TypeError, ValueError, RuntimeError), match="router"):
+        layer(half(3, 256))

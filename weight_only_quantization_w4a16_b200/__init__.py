@@ -879,6 +879,8 @@ class AWQMoE:
         return cls(router, gate_up, down, I2 // 2, top_k, renormalize, h_scale, s)
 
     def __call__(self, x, y=None, workspace=None, scaled: bool = False):
+        # the weights were checked, on one device, when the layer was made; x has to be on that device
+        _need(self.router, _torch().float16, "router", 2)
         _validate_moe_tokens(x, y, self.E, self.K)
         if self.s is not None and not scaled:
             x = awq_scale_activations(x, self.s)
