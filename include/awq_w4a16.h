@@ -24,6 +24,11 @@
  *   a3  awq_w4a16_gemv        y[M,N] = x'[M,K] . ((q - z) * S)^T, M <= 32  (fp32 accumulate, fp16 out)
  *   a4  awq_w4a16_gemm        the same for any M (tensor-core prefill kernel);
  *       awq_gemm_plan         its launch plan for a shape (token tile, K split)
+ * Beside the path:
+ *       awq_quantize_tokens, awq_quantize_channels, awq_w8a8_linear, awq_w8a8_forward
+ *                             linear layers in 8-bit integers
+ *       awq_residual_norm     residual update and RMS norms between two blocks, with the next layer's 1/s
+ *       awq_moe_w4a16         a mixture-of-experts layer for a few tokens, experts in packed weights
  *
  * Conventions for every entry point:
  *   - All data pointers are DEVICE pointers owned by the caller. The library
@@ -349,7 +354,9 @@ AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residu
  *   h_scale fp32 [E, I] or NULL (1): the down layers' s.   y fp16 [T, K].
  *   workspace: device, 16-byte aligned, awq_moe_workspace_bytes bytes; its contents before the call
  *           do not matter. Calls that may overlap on the GPU need workspaces of their own.
- * Only the chosen experts' weights are read. A logit that is NaN ranks below every number.
+ * Only the chosen experts' weights are read. A logit that is NaN ranks below every number; a token's
+ * output is NaN if it has an infinite largest logit, a NaN one among the chosen, or, without renormalize,
+ * a NaN one at all. Other tokens of the call are not affected.
  * One kernel, a cooperative launch with one CTA on every SM that waits (bounded, AWQ_ERR_TIMEOUT) for
  * all others after the router and after each of the two layers. Bitwise reproducible.
  * Requires 1 <= T <= 32, 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I multiples of 128, each

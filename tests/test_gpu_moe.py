@@ -316,3 +316,17 @@ def test_refusals_on_the_device():
         layer(x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="CUDA"):
         layer(x.cpu())
+
+
+def test_nan_logits_rank_below_every_number():
+    for renorm in (True, False):
+        c = Case(6, 40, 3, 256, 128, renorm)
+        c.x = np.abs(c.x)
+        c.router[5] = -0.05                  # far below the other logits: chosen by no token
+        last = host(c.layer()(dev(c.x)))
+        c.router[5] = np.nan
+        y = host(c.layer()(dev(c.x)))
+        if renorm:                           # the sum is over the chosen experts
+            assert np.array_equal(y, last) and np.isfinite(y).all()
+        else:
+            assert np.isnan(y).all()

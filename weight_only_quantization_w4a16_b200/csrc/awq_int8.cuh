@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
         mbar_wait_bounded(&full[i % S], static_cast<uint32_t>((i / S) & 1), &never, kDrainBudgetNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    pdl_wait();                                // its waits' budget starts with the tokens' copies
     constexpr uint32_t idesc = idesc_s8_s32(128, BT);
     const uint64_t desc_hi = smem_desc_sw128(0) & ~0xFFFFFFFFull;
     const uint32_t desc_lo = static_cast<uint32_t>(smem_desc_sw128(base));
