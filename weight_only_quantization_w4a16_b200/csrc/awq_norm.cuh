@@ -13,8 +13,9 @@
 // by latency and take as many threads as they have 8-value chunks; many rows two chunks per thread,
 // four where the norm after the block adds a second reduction and many rows hide it.
 // Measured: 8192 x 8192 83 us (0.98 of the copy rate; 95 with the IEEE division by s), 90 us with the
-// norm after the block (98 with two chunks per thread); 1023 x 11016 with a gate per token 20 us (0.84);
-// 1 x 4096 2.1 us.
+// norm after the block (98 with two chunks per thread); 4096 x 8192 with both norms and a gate per token
+// 63 us (0.81), 68 without the gate's prefetch, which a few rows of one chunk per thread do not repay
+// (300 x 4096 5.3 us, 5.7 with it); 1 x 4096 2.1 us.
 #pragma once
 
 #include "awq_common.cuh"
@@ -88,6 +89,14 @@ __global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kerne
   }
   float rstd = 1.0f;
   if (a.post_w != nullptr) {
+    if (VPT > 1 && a.gate != nullptr) {        // the gate is on its way into L2 during the reduction
+      const __half* g = a.gate + row / a.rows_per_gate * a.K;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = tid + i * nthr;
+        if (c < chunks && (c & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(g + c * 8));
+      }
+    }
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
