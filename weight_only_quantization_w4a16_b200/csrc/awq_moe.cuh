@@ -17,16 +17,21 @@
 // they get. An expert with more than 8 tokens has several blocks, whose weights come from L2 after the
 // first: each block's activation fragments then fit a warp's registers. Phase 2 goes through partial
 // sums so that its units are as many and as small as phase 1's and a warp keeps its fragments along the
-// tiles; summing all blocks of a tile in one CTA left it at 59% of the HBM rate where phase 1 has 87%.
+// tiles; summing all blocks of a tile in one CTA left it at 59% of the HBM rate.
 //
 // Per CTA: a producer lane streams both phases' packed weights through one ring of shared memory
 // without waiting for the barrier, so phase 2's first weights arrive while phase 1 ends. A stage holds
 // 16 (tile, group pair) items of each of two tiles, one of each for each of the 16 consumer warps, which so
 // split the tiles' K. A warp's activation fragments stay in registers while it walks along the tiles of a
-// block. Each warp
-// leaves its sums of a tile in shared memory, and epilogue warps add them in warp order and apply SiLU,
-// the weight p and the rounding: results repeat bit for bit. h carries p: its fp16 rounding (2^-12 of
-// each term on average) is the one that unfused layers make between their calls.
+// block. Each warp leaves its sums of a tile in shared memory, and epilogue warps add them in warp order
+// and apply SiLU, the weight p and the rounding: results repeat bit for bit. h carries p: its fp16
+// rounding (2^-11 relative at most) is the one that unfused layers make between their calls.
+//
+// Measured (8 experts of 4096 x 14336, two per token): 1 token 51 us, of which 28 are the HBM time of the
+// weights and 15 to 18 the router, three barriers (1.3 to 2 us each) and the first and last stages; 8
+// tokens 133 (floor 99; phase 1 at 96% of the HBM rate, phase 2 at 80%); 32 tokens 205 (floor 112), bound
+// by the consumers' instructions on the experts' second blocks. 64 experts of 2048 x 1408, six per token,
+// 5 tokens: 42 (floor 17).
 //
 // The kernel neither starts before its predecessor has ended nor lets its successor start early: CTAs
 // that wait for it could otherwise hold the registers that its own last CTAs need, and the barrier
