@@ -237,3 +237,15 @@ def test_two_streams_at_once():
         check_y(y, ref)
     assert all(torch.equal(a[0], b[0]) for a, b in zip(out[::2], out[2::2]))
     assert P.awq_poll_device_status() == P.AWQ_OK
+
+
+# On 148 SMs these take the remaining combinations of token tile, weight rows per tile and K split: 16 to 64
+# columns with tiles of 256 rows, 1 to 8 CTAs a tile, and 128 and 256 columns with K split 2 and 4 ways
+FORMS = [(1, 130, 528), (1, 25, 528), (19, 25, 16), (19, 130, 1040), (19, 38001, 80), (19, 25, 1040), (41, 25, 16),
+         (41, 38001, 144), (41, 25, 528), (41, 25, 1040), (70, 5001, 4112), (70, 2305, 8208), (199, 5001, 14352),
+         (199, 2305, 14352)]
+
+
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_product_forms(M, N, K):
+    test_product(M, N, K)
