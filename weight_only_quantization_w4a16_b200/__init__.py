@@ -161,24 +161,26 @@ def _torch():
 _raw_stream = None     # current stream handle of a device, without building a Stream object where torch allows it
 
 
-def _stream_ptr():
+def _stream_ptr(device=None):
+    """The current stream's handle on `device`, the current one where the caller does not know it already."""
     global _raw_stream
-    torch = _torch()
     if _raw_stream is None:
+        torch = _torch()
         torch.cuda.init()
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_torch().cuda.current_device() if device is None else device)
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _fits(t, dtype, shape, device: int) -> bool:
-    """Whether t is a contiguous tensor of this type and shape on the given (current) device: what the
+def _fits(t, dtype, dims: int, numel: int, device: int) -> bool:
+    """Whether t is a contiguous tensor of this type and size on the given (current) device: what the
     validators check, without their messages. The calls that are made once per token ask this first."""
-    return type(t) is _torch_mod.Tensor and t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+    return (type(t) is _torch_mod.Tensor and t.dtype is dtype and t.dim() == dims and t.numel() == numel and
+            t.get_device() == device and t.is_contiguous())
 
 
 def _need(t, dtype, name, dims=None, require_cuda=True):
@@ -636,8 +638,8 @@ class AWQInt8Linear:
         # the weights were checked when the layer was made; they and x have to be on the current device
         torch = _torch()
         dev = torch.cuda.current_device()
-        if (y is None and type(x) is torch.Tensor and x.dim() == 2 and x.shape[0] > 0 and self.wq.get_device() == dev and
-                _fits(x, torch.float16, (x.shape[0], self.K), dev)):
+        if (y is None and type(x) is torch.Tensor and x.dtype is torch.float16 and x.dim() == 2 and x.shape[1] == self.K and
+                x.shape[0] > 0 and x.get_device() == dev and x.is_contiguous() and self.wq.get_device() == dev):
             return _w8a8_forward(x, self.wq, self.sw, self.s, None, workspace)
         return awq_w8a8_forward(x, self.wq, self.sw, self.s, y, workspace)
 
@@ -676,7 +678,7 @@ def _w8a8_forward(x, wq, sw, s, y, workspace):
     elif _need(workspace, wq.dtype, "workspace", 1) is None and workspace.numel() < need:
         raise ValueError(f"workspace must hold {need} bytes")
     if y is None:
-        y = x.new_empty((M, N))
+        y = x.new_empty(M, N)
     st = lib.awq_w8a8_forward(x.data_ptr(), _ptr(s), wq.data_ptr(), sw.data_ptr(), y.data_ptr(), M, N, K,
                               workspace.data_ptr(), need, _stream_ptr())
     if st:
@@ -736,21 +738,24 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
             raise ValueError("x is always written")
     alpha, eps = float(alpha), float(eps)
     dev, f16 = torch.cuda.current_device(), torch.float16
-    shape = y.shape if type(y) is torch.Tensor else ()
-    if not (out is None and gate is None and post_weight is None and len(shape) == 2 and _fits(y, f16, shape, dev) and
-            0 < shape[0] and 8 <= shape[1] <= NORM_MAX_K and shape[1] % 8 == 0 and
-            (residual is None or _fits(residual, f16, shape, dev)) and _fits(weight, f16, shape[1:], dev) and
-            (s is None or _fits(s, torch.float32, shape[1:], dev)) and -3.0e38 <= alpha <= 3.0e38 and 0.0 <= eps <= 3.0e38):
+    fits = (out is None and gate is None and post_weight is None and type(y) is torch.Tensor and y.dtype is f16 and
+            y.dim() == 2 and y.get_device() == dev and y.is_contiguous())
+    if fits:
+        M, K = shape = y.shape
+        fits = (0 < M and 8 <= K <= NORM_MAX_K and K % 8 == 0 and _fits(weight, f16, 1, K, dev) and
+                (residual is None or (_fits(residual, f16, 2, M * K, dev) and residual.shape == shape)) and
+                (s is None or _fits(s, torch.float32, 1, K, dev)) and -3.0e38 <= alpha <= 3.0e38 and 0.0 <= eps <= 3.0e38)
+    if not fits:
         validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
+        M, K = y.shape
     if out is None:
         x = torch.empty_like(y)
         if want_h:
             h = torch.empty_like(y)
-    M, K = shape
     per = M // gate.shape[0] if gate is not None else 1
     st = load_library().awq_residual_norm(y.data_ptr(), _ptr(residual), _ptr(gate), per, _ptr(post_weight),
                                           weight.data_ptr(), _ptr(s), alpha, eps, M, K, _ptr(h), x.data_ptr(),
-                                          _stream_ptr())
+                                          _stream_ptr(dev))
     if st:
         _check("awq_residual_norm", st)
     return h, x
