@@ -162,3 +162,14 @@ def test_refusals_on_the_device():
                             ((None, y, w), {}, TypeError), ((y, y, None), {}, TypeError)):
         with pytest.raises(error):
             P.awq_residual_norm(*args, **kw)
+
+
+def test_gate_and_post_weight_refusals_on_the_device():
+    torch, P = torch_mod(), lib()
+    half = lambda *shape: torch.ones(shape, dtype=torch.float16, device="cuda")  # noqa: E731
+    y = half(4, 64)
+    for bad in (dict(gate=half(3, 64)), dict(gate=half(0, 64)), dict(gate=half(2, 72)), dict(gate=half(64)),
+                dict(gate=half(2, 64).float()), dict(gate=half(64, 2).t()), dict(gate=half(2, 64).cpu()),
+                dict(post_weight=half(63)), dict(post_weight=half(1, 64)), dict(post_weight=half(64).float())):
+        with pytest.raises((ValueError, TypeError)):
+            P.awq_residual_norm(y, y, half(64), **bad)

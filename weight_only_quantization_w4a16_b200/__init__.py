@@ -738,13 +738,16 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
             raise ValueError("x is always written")
     alpha, eps = float(alpha), float(eps)
     dev, f16 = torch.cuda.current_device(), torch.float16
-    fits = (out is None and gate is None and post_weight is None and type(y) is torch.Tensor and y.dtype is f16 and
-            y.dim() == 2 and y.get_device() == dev and y.is_contiguous())
+    fits = (out is None and type(y) is torch.Tensor and y.dtype is f16 and y.dim() == 2 and y.get_device() == dev and
+            y.is_contiguous())
     if fits:
         M, K = shape = y.shape
         fits = (0 < M and 8 <= K <= NORM_MAX_K and K % 8 == 0 and _fits(weight, f16, 1, K, dev) and
                 (residual is None or (_fits(residual, f16, 2, M * K, dev) and residual.shape == shape)) and
-                (s is None or _fits(s, torch.float32, 1, K, dev)) and -3.0e38 <= alpha <= 3.0e38 and 0.0 <= eps <= 3.0e38)
+                (s is None or _fits(s, torch.float32, 1, K, dev)) and
+                (post_weight is None or _fits(post_weight, f16, 1, K, dev)) and
+                (gate is None or (type(gate) is torch.Tensor and _fits(gate, f16, 2, gate.numel(), dev) and
+                                  gate.shape[1] == K and gate.shape[0] > 0 and M % gate.shape[0] == 0)) and -3.0e38 <= alpha <= 3.0e38 and 0.0 <= eps <= 3.0e38)
     if not fits:
         validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
         M, K = y.shape
