@@ -345,8 +345,9 @@ AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residu
 /* A whole mixture-of-experts layer for a few tokens (decode), experts in packed 4-bit weights:
  *   l_te = sum_k x_tk router_ek (fp32); the top_k experts of token t by l, ties to the lowest index;
  *   p_te = softmax over all E experts of l_t at the chosen ones, divided by their sum if renormalize;
- *   h    = p_te * SiLU(x_t . Wgate_e^T) * (x_t . Wup_e^T) / h_scale_e      (fp32, rounded to fp16)
- *   y_t  = sum over the chosen e of h . Wdown_e^T                          (fp32 sums, fp16 output)
+ *   h    = SiLU(x_t . Wgate_e^T) * (x_t . Wup_e^T) / h_scale_e             (fp32)
+ *   y_t  = sum over the chosen e of p_te * (h . Wdown_e^T)                 (fp32 sums, fp16 output)
+ * with each h taken to within 2^-20 of the largest of the token's 256 in its pair of groups.
  *   x       fp16 [T, K], already divided by the gate/up layers' s (awq_scale_activations,
  *           awq_residual_norm); router fp16 [E, K], multiplied by the same s.
  *   gate_up E packed layers of 2*I x K (I gate rows, then I up rows) in packed layout v2, one after
@@ -356,7 +357,7 @@ AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residu
  *           do not matter. Calls that may overlap on the GPU need workspaces of their own.
  * Only the chosen experts' weights are read. A logit that is NaN ranks below every number; a token's
  * output is NaN if it has an infinite largest logit, a NaN one among the chosen, or, without renormalize,
- * a NaN one at all. Other tokens of the call are not affected.
+ * a NaN one at all, or if one of its h is NaN or past fp32's range. Other tokens of the call are not affected.
  * One kernel, a cooperative launch with one CTA on every SM that waits (bounded, AWQ_ERR_TIMEOUT) for
  * all others after the router and after each of the two layers. Bitwise reproducible.
  * Requires 1 <= T <= 32, 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I multiples of 128, each

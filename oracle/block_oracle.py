@@ -74,10 +74,9 @@ def route(x, router, top, renormalize):
 def moe(x, router, gate_up, down, top, renormalize, h_scale=None):
     """(y, bound) of the layer with dequantized experts gate_up [E, 2I, K], down [E, K, I].
 
-    bound: the error that the definition's roundings allow. h is rounded to fp16 (half a step, 2^-11,
-    or 2^-25 below the normal range); sums of products in fp32 on tensor cores are taken as off by at
-    most 2^-18 of the sum of magnitudes, p, SiLU and the division by h_scale as off by 2^-18; y is
-    rounded to fp16 at the end."""
+    bound: the error that the definition's roundings allow. Sums of products in fp32 on tensor cores are
+    taken as off by at most 2^-18 of the sum of magnitudes, p, SiLU and the division by h_scale as off by
+    2^-16; h as off by 2^-20 of its largest value; y is rounded to fp16 at the end."""
     x = np.asarray(x, f64)
     I = down.shape[2]
     ids, p, gap = route(x, router, top, renormalize)
@@ -91,7 +90,7 @@ def moe(x, router, gate_up, down, top, renormalize, h_scale=None):
             sig = 1.0 / (1.0 + np.exp(-np.clip(g, -700, 700)))
             slope = np.abs(sig * (1.0 + g * (1.0 - sig)))
             dh = w / s * 2.0 ** -18 * (slope * np.abs(u) * mag[:I] + np.abs(silu(g)) * mag[I:])
-            dh = dh + np.abs(h) * (2.0 ** -16 + 2.0 ** -11) + 2.0 ** -25
+            dh = dh + np.abs(h) * 2.0 ** -16 + np.abs(h).max() * 2.0 ** -20
             a = np.abs(down[e])
             y[t] += down[e] @ h
             err[t] += a @ dh + 2.0 ** -18 * (a @ np.abs(h))

@@ -753,7 +753,7 @@ MoeWs moe_ws(int T, int E, int K, int I, int top) {
   const size_t slots = static_cast<size_t>(T) * top;
   size_t o = 0;
   w.logits = o; o = align256(o + static_cast<size_t>(T) * E * 4);
-  w.h = o; o = align256(o + slots * I * 2);
+  w.h = o; o = align256(o + slots * I * 4);
   w.part = o; o = align256(o + slots * MoeCut((I / kGroup + 1) / 2).chunks * K * 4);
   w.total = o;
   return w;
@@ -1190,7 +1190,7 @@ awq_status_t awq_moe_w4a16(const uint16_t* x, const uint16_t* router, const uint
   a.h_scale = h_scale;
   a.router = reinterpret_cast<const __half*>(router);
   a.logits = reinterpret_cast<float*>(ws + w.logits);
-  a.h = reinterpret_cast<__half*>(ws + w.h);
+  a.h = reinterpret_cast<float*>(ws + w.h);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.y = reinterpret_cast<__half*>(y);
   a.T = T; a.E = E; a.K = K; a.I = I; a.top = top_k;

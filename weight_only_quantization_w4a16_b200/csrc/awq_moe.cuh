@@ -3,8 +3,8 @@
 //
 //   l_te = x_t . Wr_e              the top_k experts of token t by l (ties: lowest index)
 //   p_te = exp(l_te - max) / sum   the sum over all experts, or over the chosen ones (renormalize)
-//   h    = p_te * SiLU(x_t . Wg_e^T) * (x_t . Wu_e^T) [/ s_e]          (fp16)
-//   y_t  = sum over the chosen e of h . Wd_e^T
+//   h    = SiLU(x_t . Wg_e^T) * (x_t . Wu_e^T) [/ s_e]                 (fp32)
+//   y_t  = sum over the chosen e of p_te * (h . Wd_e^T)
 //
 // The layer is bound by the packed weights of the experts that are chosen at all (0.52 bytes per
 // weight). One CTA per SM, launched cooperatively, in four phases with a grid-wide barrier between:
@@ -24,14 +24,17 @@
 // 16 (tile, group pair) items of each of two tiles, one of each for each of the 16 consumer warps, which so
 // split the tiles' K. A warp's activation fragments stay in registers while it walks along the tiles of a
 // block. Each warp leaves its sums of a tile in shared memory, and epilogue warps add them in warp order
-// and apply SiLU, the weight p and the rounding: results repeat bit for bit. h carries p: its fp16
-// rounding (2^-11 relative at most) is the one that unfused layers make between their calls.
+// and apply SiLU (phase 1) or the weight p (phase 2): results repeat bit for bit. h stays in fp32 and enters
+// phase 2 as 21-bit integers with a power of two per token and 256 values (MoeInts), so y's rounding is the
+// only one to fp16.
 //
-// Measured (8 experts of 4096 x 14336, two per token): 1 token 51 us, of which 28 are the HBM time of the
-// weights and 15 to 18 the router, three barriers (1.3 to 2 us each) and the first and last stages; 8
-// tokens 133 (floor 99; phase 1 at 96% of the HBM rate, phase 2 at 80%); 32 tokens 205 (floor 112), bound
-// by the consumers' instructions on the experts' second blocks. 64 experts of 2048 x 1408, six per token,
-// 5 tokens: 42 (floor 17).
+// Measured (8 experts of 4096 x 14336, two per token): 1 token 54 us, of which 28 are the HBM time of the
+// weights and 17 to 20 the router, three barriers (1.3 to 2 us each), the first and last stages and the
+// integers of h; 8 tokens 144 (floor 96); 32 tokens 212 to 218 (floor 112), bound by the consumers'
+// instructions, of which every block of 8 tokens has its own. 64 experts of 2048 x 1408, six per token, 5
+// tokens: 46 (floor 17). A warp's integers of h take 1300 to 2000 cycles each time it comes to another block
+// or part of K, which h in fp16 did in half of that (51, 138, 205 and 42 us): its rounding doubled the
+// output's squared error, and what lies below 2^-14 lost more, down to all of it.
 //
 // The kernel neither starts before its predecessor has ended nor lets its successor start early: CTAs
 // that wait for it could otherwise hold the registers that its own last CTAs need, and the barrier
@@ -57,7 +60,7 @@ struct MoeArgs {
   size_t gu_pairs, dn_pairs;                   // (tile, group pair) items of one expert's layer
   const float* h_scale;                        // [E, I] or null
   float* logits;                               // [T, E]
-  __half* h;                                   // [T * top, I]
+  float* h;                                    // [T * top, I]
   float* part;                                 // [T * top, chunks of I, K]
   __half* y;                                   // [T, K]
   int T, E, K, I, top, renorm;
@@ -238,6 +241,64 @@ __device__ __forceinline__ void moe_products(float (&acc)[4], const MoeItem& m, 
       }
 #pragma unroll
   for (int g = 0; g < 2; ++g) moe_scale(acc, tq[g], f.s[g], m.s[g], m.z[g]);
+}
+
+// h is fp32 and enters phase 2 as integers: a token's 256 values of a group pair are H / 2^(19 - e), e the
+// exponent of the largest magnitude and H = rint(h 2^(19 - e)), |H| <= 2^20, so that each is off by at most
+// 2^-20 of the largest. The sums of (q - z) H are exact: |sum| <= 15 * 128 * 2^20 < 2^31. H's three bytes
+// are the operands of three products with the codes as bytes: mma.sync in 8-bit integers takes 32 k in the
+// two cycles in which fp16 takes 16 (measured per SM), and the codes of 32 k four ANDs and two shifts, half
+// of what fp16 operands take. h as a sum of two fp16 values needs two products of that kind and 32 registers
+// more, which spill: 22% of the call at 8 tokens over fp16 alone (123 to 150 us), where the integers cost 6%
+// (136 to 144).
+struct MoeInts {
+  uint32_t v[3][2][2][4];   // [byte of H, highest first][group][64-k tile][4 k]
+  uint32_t s[2][2];         // sum of H: [group][column 2t, 2t+1]
+  float inv[2];             // 2^(e - 19) of the columns; NaN where a value is not finite
+};
+
+// D = A . B + C, A unsigned bytes, B signed or unsigned bytes, int32.
+template <bool SIGNED>
+__device__ __forceinline__ void mma_m16n8k32_i32(uint32_t (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                                 const uint32_t (&c)[4]) {
+  if (SIGNED)
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
+  else
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]));
+}
+
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
+
+// acc += S sum (q - z) H of one group (w: its two 64-k tiles). A word's low nibbles are row r at k, k+2, k+1,
+// k+3, its high nibbles row r + 8.
+__device__ __forceinline__ void moe_int_products(float (&acc)[4], const uint4 (&w)[2], uint32_t sv, uint32_t zz, const MoeInts& f, int g) {
+  uint32_t d[3][4] = {};
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t q0 = j ? w[kt].z : w[kt].x, q1 = j ? w[kt].w : w[kt].y;
+      const uint32_t a[4] = {q0 & 0x0F0F0F0Fu, (q0 >> 4) & 0x0F0F0F0Fu, q1 & 0x0F0F0F0Fu, (q1 >> 4) & 0x0F0F0F0Fu};
+      mma_m16n8k32_i32<true>(d[0], a, f.v[0][g][kt][2 * j], f.v[0][g][kt][2 * j + 1], d[0]);
+      mma_m16n8k32_i32<false>(d[1], a, f.v[1][g][kt][2 * j], f.v[1][g][kt][2 * j + 1], d[1]);
+      mma_m16n8k32_i32<false>(d[2], a, f.v[2][g][kt][2 * j], f.v[2][g][kt][2 * j + 1], d[2]);
+    }
+  const float2 sc = half2_bits_to_float2(sv);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {                // modulo 2^32 on the way, in range at the end
+    const uint32_t z = j < 2 ? zz & 15u : zz >> 4;
+    const uint32_t v = (((d[0][j] << 8) + d[1][j]) << 8) + d[2][j] - z * f.s[g][j & 1];
+    acc[j] = fmaf(j < 2 ? sc.x : sc.y, static_cast<float>(static_cast<int>(v)), acc[j]);
+  }
 }
 
 __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a) {
@@ -468,8 +529,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 
   if (warp > kMoeCW) {
     // ---------------------------------------------------------------- epilogue warps
-    // the sum of the records of warps w0..w0+nw-1, without the factors that the codes carry (row r: 2^-24,
-    // row r + 8: 2^-20)
+    // the sum of the records of warps w0..w0+nw-1
     auto sum = [&](int half, int w0, int nw, int col, int row) {
       const float* p = rec_of(w0, half) + col * 20 + row;
       float v = 0.0f;
@@ -479,7 +539,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       } else {
         for (int w = 0; w < nw; ++w) v += p[w * 2 * kMoeRec];
       }
-      return v * (row < 8 ? 16777216.0f : 1048576.0f);
+      return v;
     };
     const int lane0 = 32 * (warp - kMoeCW - 1) + lane;
     bool ok = true;
@@ -496,10 +556,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
               const int row = q & 15, i = (q >> 4) & (k1.strips - 1), col = q >> (4 + k1.shift);
               const int i_row = 16 * (what.y + i) + row;
               if (i >= nu || !AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
-              const float g = sum(0, i * k1.wide, k1.len, col, row), v = sum(1, i * k1.wide, k1.len, col, row);
-              float hv = silu_mul(g, v) * l_p[first + col];
+              const float code = row < 8 ? 16777216.0f : 1048576.0f;           // the factors that the codes carry
+              const float g = code * sum(0, i * k1.wide, k1.len, col, row), v = code * sum(1, i * k1.wide, k1.len, col, row);
+              float hv = silu_mul(g, v);
               if (a.h_scale != nullptr) hv = __fdiv_rn(hv, __ldg(a.h_scale + static_cast<size_t>(l_expert[x]) * a.I + i_row));
-              a.h[static_cast<size_t>(first + col) * a.I + i_row] = __float2half_rn(hv);
+              a.h[static_cast<size_t>(first + col) * a.I + i_row] = hv;
             }
           } else {
             const int nw = min(k2.len, k2.Q - what.w * k2.len);
@@ -507,7 +568,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
               const int row = q & 15, i = (q >> 4) & (k2.strips - 1), half = (q >> (4 + k2.shift)) & 1, col = q >> (5 + k2.shift);
               const int k = 16 * (half * (a.K / 32) + what.y + i) + row;
               if (i >= nu || !AWQ_CHECK(first + col < n_assign && k < a.K)) continue;
-              a.part[(static_cast<size_t>(first + col) * k2.chunks + what.w) * a.K + k] = sum(half, i * k2.wide, nw, col, row);
+              a.part[(static_cast<size_t>(first + col) * k2.chunks + what.w) * a.K + k] =
+                  l_p[first + col] * sum(half, i * k2.wide, nw, col, row);
             }
           }
         }
@@ -559,35 +621,117 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
       f.s[g][1] = d[1];
     }
   };
-  float* const rec0 = rec + warp * 2 * kMoeRec + 2 * t * 20 + r;               // this lane's place in a record
+  // The same of h; `row` is fp32.
+  auto load_ints = [&](MoeInts& f, const float* row, int pr, int G) {
+    float v[2][2][4][4];
+    float top = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 w = 2 * pr + g < G ? ld_coherent_v4(row + pr * 256 + g * 128 + kk * 64 + 16 * t + 4 * i)
+                                         : make_uint4(0, 0, 0, 0);   // the padding group
+          v[g][kk][i][0] = __uint_as_float(w.x);
+          v[g][kk][i][1] = __uint_as_float(w.y);
+          v[g][kk][i][2] = __uint_as_float(w.z);
+          v[g][kk][i][3] = __uint_as_float(w.w);
+        }
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top = max_abs_nan(top, v[g][kk][i][0], v[g][kk][i][1]);
+          top = max_abs_nan(top, v[g][kk][i][2], v[g][kk][i][3]);
+        }
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
+    top = max_abs_nan(top, other, other);
+    const float others = __shfl_xor_sync(0xFFFFFFFFu, top, 2);               // the four lanes of a token
+    const uint32_t bits = __float_as_uint(max_abs_nan(top, others, others)) & 0x7FFFFFFFu;
+    const uint32_t e = max(bits >> 23, 27u);   // 127 more than the exponent; values below 2^-100 go by that one
+    const float scale = __uint_as_float((273u - e) << 23);     // 2^(19 - exponent)
+    const float inv = bits >= 0x7F800000u ? NAN : __uint_as_float((e - 19u) << 23);
+    f.inv[0] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t);
+    f.inv[1] = __shfl_sync(0xFFFFFFFFu, inv, 8 * t + 4);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // 1.5 2^23 + H: H, rounded half to even, in the low bits; plus 64 in byte 2
+          uint32_t n[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) n[c] = __float_as_uint(fmaf(v[g][kk][i][c], scale, 12582912.0f));
+          sum += n[0] + n[1];
+          sum += n[2] + n[3];
+          const uint32_t p = __byte_perm(n[0], n[2], 0x5140), q = __byte_perm(n[1], n[3], 0x5140);   // in the codes' order
+          const uint32_t hi = __byte_perm(__byte_perm(n[0], n[2], 0x0062), __byte_perm(n[1], n[3], 0x0062), 0x5410);
+          f.v[0][g][kk][i] = (hi ^ 0x40404040u) | (~(hi << 1) & 0x80808080u);      // less 64, from 48..80
+          f.v[1][g][kk][i] = __byte_perm(p, q, 0x7632);
+          f.v[2][g][kk][i] = __byte_perm(p, q, 0x5410);
+        }
+      sum -= 32u * 0x4B400000u;
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      f.s[g][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t);
+      f.s[g][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4);
+    }
+  };
+  // Waits for the stage that `slot` names; whether there is one, and in `what` its content.
+  auto next_stage = [&](int4& what) -> bool {
+    if (!warp_wait(&full[slot], phase)) return false;
+    what = stage_of[slot];
+    return true;
+  };
+  auto release_stage = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[slot]);
+    advance();
+  };
+  auto put = [&](int half, float v0, float v1, float v2, float v3) {
+    float* p = rec + rbuf * (kMoeCW * 2 * kMoeRec) + (2 * warp + half) * kMoeRec + 2 * t * 20 + r;
+    p[0] = v0;
+    p[20] = v1;
+    p[8] = v2;
+    p[28] = v3;
+  };
+  auto announce = [&](const int4& what) {
+    if (threadIdx.x == 0) event_of[rbuf] = what;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&rfull[rbuf]);
+    next_event();
+  };
+  // columns past a block's last token repeat it; they are never used
+  auto slot_of = [&](int x) { return l_first[x] + min(r, l_first[x + 1] - l_first[x] - 1); };
   const uint8_t* const item0 = smem + lane * 16;
-  bool ok = true;
-  for (int ph = 0; ph < 2; ++ph) {
-    const int G = (ph ? a.I : a.K) / kGroup;
-    const int Q = ph ? k2.Q : k1.Q, len = ph ? k2.len : k1.len, wide = ph ? k2.wide : k1.wide;
-    const int last = ph ? 0 : k1.chunks - 1;   // the chunk that completes a unit (phase 2: any)
-    const int pl = warp % wide, sub = warp / wide;
-    const int item = sub * Q + pl;             // of a stage with several strips, one after another
-    const int oc = item * kPairCodeBytes, os = kMoeOffS + item * kPairScaleBytes + (r - 4 * lane) * 4,
-              oz = kMoeOffZ + item * kPairZeroBytes + r - 16 * lane;           // from item0
+  auto load_item = [&](uint4 (&w)[2], uint32_t& sv, uint32_t& zz, const uint8_t* sb, int item, int h, int g) {
+    const uint8_t* c = sb + (item + h * kMoeTile) * kPairCodeBytes + g * 1024;
+    w[0] = *reinterpret_cast<const uint4*>(c);
+    w[1] = *reinterpret_cast<const uint4*>(c + 512);
+    sv = *reinterpret_cast<const uint32_t*>(sb + kMoeOffS + (item + h * kMoeTile) * kPairScaleBytes + g * 32 + (r - 4 * lane) * 4);
+    zz = sb[kMoeOffZ + (item + h * kMoeTile) * kPairZeroBytes + g * 8 + r - 16 * lane];
+  };
+  auto phase1 = [&]() -> bool {
+    const int pl = warp % k1.wide, sub = warp / k1.wide;
+    const int item = sub * k1.Q + pl;          // of a stage with several strips, one after another
     float acc[2][4] = {};                      // the unit's two tiles
     MoeFrag f;
     int fx = -1, fc = 0;                       // block and chunk of the fragments
     bool mine = false;                         // whether the warp has a pair of the chunk
     while (true) {
-      ok = warp_wait(&full[slot], phase);
-      if (!ok) break;
-      const int4 what = stage_of[slot];
+      int4 what;
+      if (!next_stage(what)) return false;
       if (what.z > 0) {
         if (what.x != fx || what.w != fc) {
           fx = what.x;
           fc = what.w;
-          const int pr = fc * len + pl;
-          mine = pl < len && pr < Q;
-          // columns past the block's last token repeat it; they are never used
-          const int first = l_first[fx], s = first + min(r, l_first[fx + 1] - first - 1);
-          const __half* row = ph ? a.h + static_cast<size_t>(s) * a.I : a.x + static_cast<size_t>(l_token[s]) * a.K;
-          if (mine) load_frag(f, row, pr, G);
+          mine = pl < k1.len && fc * k1.len + pl < k1.Q;
+          if (mine) load_frag(f, a.x + static_cast<size_t>(l_token[slot_of(fx)]) * a.K, fc * k1.len + pl, a.K / kGroup);
         }
         if (mine && sub < what.z) {
           const uint8_t* sb = item0 + slot * kMoeStage;
@@ -595,39 +739,65 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
           for (int h = 0; h < 2; ++h) {
             MoeItem m;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              m.w[g][0] = *reinterpret_cast<const uint4*>(sb + oc + h * kMoeTile * kPairCodeBytes + g * 1024);
-              m.w[g][1] = *reinterpret_cast<const uint4*>(sb + oc + h * kMoeTile * kPairCodeBytes + g * 1024 + 512);
-              m.s[g] = *reinterpret_cast<const uint32_t*>(sb + os + h * kMoeTile * kPairScaleBytes + g * 32);
-              m.z[g] = sb[oz + h * kMoeTile * kPairZeroBytes + g * 8];
-            }
+            for (int g = 0; g < 2; ++g) load_item(m.w[g], m.s[g], m.z[g], sb, item, h, g);
             moe_products(acc[h], m, f);
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[slot]);
-      advance();
-      if (what.z > 0 && ph == 0 && what.w != last) continue;   // the unit's sums go on
-      ok = warp_wait(&rempty[rbuf], rphase ^ 1);
-      if (!ok) break;
-      float* p = rec0 + rbuf * (kMoeCW * 2 * kMoeRec);
+      release_stage();
+      if (what.z > 0 && what.w != k1.chunks - 1) continue;   // the unit's sums go on
+      if (!warp_wait(&rempty[rbuf], rphase ^ 1)) return false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        p[h * kMoeRec] = acc[h][0];
-        p[h * kMoeRec + 20] = acc[h][1];
-        p[h * kMoeRec + 8] = acc[h][2];
-        p[h * kMoeRec + 28] = acc[h][3];
+        put(h, acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
         acc[h][0] = acc[h][1] = acc[h][2] = acc[h][3] = 0.0f;
       }
-      if (threadIdx.x == 0) event_of[rbuf] = what;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rfull[rbuf]);
-      next_event();
-      if (what.z == 0) break;
+      announce(what);
+      if (what.z == 0) return warp_wait(go, 0);
     }
-    ok = ok && warp_wait(go, ph);
-  }
+  };
+  auto phase2 = [&]() -> bool {                // every stage completes its units
+    const int pl = warp % k2.wide, sub = warp / k2.wide;
+    const int item = sub * k2.Q + pl;
+    MoeInts f;
+    int fx = -1, fc = 0;
+    bool mine = false;
+    while (true) {
+      int4 what;
+      if (!next_stage(what)) return false;
+      if (what.z > 0 && (what.x != fx || what.w != fc)) {
+        fx = what.x;
+        fc = what.w;
+        mine = pl < k2.len && fc * k2.len + pl < k2.Q;
+        if (mine) load_ints(f, a.h + static_cast<size_t>(slot_of(fx)) * a.I, fc * k2.len + pl, a.I / kGroup);
+      }
+      if (!warp_wait(&rempty[rbuf], rphase ^ 1)) return false;
+      const bool has = mine && sub < what.z;
+      const uint8_t* sb = item0 + slot * kMoeStage;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float acc[4] = {};
+        if (has) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint4 w[2];
+            uint32_t sv, zz;
+            load_item(w, sv, zz, sb, item, h, g);
+            moe_int_products(acc, w, sv, zz, f, g);
+          }
+          acc[0] *= f.inv[0];
+          acc[1] *= f.inv[1];
+          acc[2] *= f.inv[0];
+          acc[3] *= f.inv[1];
+        }
+        put(h, acc[0], acc[1], acc[2], acc[3]);
+      }
+      release_stage();
+      announce(what);
+      if (what.z == 0) return warp_wait(go, 1);
+    }
+  };
+  const bool ok = phase1() && phase2();
 
   // ---- phase 3: y, four values a thread; a token's partial sums in the order of its choices and of K
   if (!ok) return;
