@@ -135,3 +135,99 @@ def test_small_and_large_intermediates(what, gu_std, dn_std, h_scale):
     y = c()
     assert bool(y.isfinite().all())
     c.check(y, what=what)
+
+
+# ---------------------------------------------------------------------------- forms
+# (T, E, top, K, I), then whether the last units are drawn in phase 1 and in phase 2, and the chunks of K that
+# they have there. 9 and 10 pairs of groups a chunk where a chunk holds up to 16; stages of one strip and of two.
+FORMS = [((17, 2, 2, 4224, 4736), (True, True), (2, 2)), ((9, 4, 4, 8192, 4096), (True, True), (2, 1)),
+         ((32, 4, 2, 4096, 14336), (True, True), (1, 4)), ((1, 3, 1, 6144, 2048), (False, False), (2, 1)),
+         ((32, 4, 4, 2048, 4736), (True, True), (1, 2)), ((32, 4, 4, 8192, 2048), (True, True), (2, 1))]
+
+
+def form(shape, blocks):
+    """((drawn in phase 1, in phase 2), (chunks of each)) by the kernel's rules for this device."""
+    _, _, _, K, I = shape
+    ctas = torch_mod().cuda.get_device_properties(0).multi_processor_count
+    (strips1, chunks1), (strips2, chunks2) = cut(K // 128), cut(I // 128)
+    drawn = (blocks * (I // 16) >= 8 * ctas * strips1, blocks * chunks2 * (K // 32) >= 8 * ctas * strips2)
+    return drawn, (chunks1, chunks2)
+
+
+@pytest.mark.parametrize("shape,drawn,chunks", FORMS)
+def test_forms(shape, drawn, chunks):
+    torch, P = torch_mod(), lib()
+    c = Layer(*shape)
+    ref = c.reference()
+    assert form(shape, ref[2]) == (drawn, chunks)
+    y = c()
+    c.check(y, ref)
+    assert all(torch.equal(y, c()) for _ in range(5))      # whoever draws a unit, the sums are the same
+    assert P.awq_poll_device_status() == P.AWQ_OK
+
+
+def test_forms_with_scales_and_without_renormalization():
+    c = Layer(17, 2, 2, 4224, 4736, renorm=False, h_scale=1.0)
+    c.check(c())
+
+
+def test_drawn_units_replayed_and_beside_another_stream():
+    """Launches that draw units follow and overlap one another: each starts from the tickets that the last left."""
+    torch, P = torch_mod(), lib()
+    c, d = Layer(17, 2, 2, 4224, 4736), Layer(9, 4, 4, 8192, 4096)
+    rc, rd = c.reference(), d.reference()
+    yc, yd = c(), d()
+    c.check(yc, rc)
+    d.check(yd, rd)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        zc, zd = c(), d()
+    for _ in range(3):
+        zc.zero_()
+        zd.zero_()
+        g.replay()
+        assert torch.equal(zc, yc) and torch.equal(zd, yd)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(12):
+        for layer, s in zip((c, d), streams):
+            with torch.cuda.stream(s):
+                out.append(layer())
+    torch.cuda.synchronize()
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    assert all(torch.equal(y, (yc, yd)[i % 2]) for i, y in enumerate(out))
+
+
+def test_drawn_units_after_a_wait_that_ran_out():
+    P = lib()
+    c = Layer(17, 2, 2, 4224, 4736)
+    ref = c.reference()
+    c.check(c(), ref)
+    for _ in range(3):
+        P.awq_debug_set_wait_budget_ns(1)
+        try:
+            c()
+            status = P.awq_poll_device_status()
+        finally:
+            P.awq_debug_set_wait_budget_ns(0)
+        assert status == P.AWQ_ERR_TIMEOUT
+        c.check(c(), ref, "after a timeout")
+        assert P.awq_poll_device_status() == P.AWQ_OK
+
+
+@pytest.mark.parametrize("shape", [s for s, _, _ in FORMS if s[4] <= 8192])
+def test_forms_in_the_bounds_checked_build(shape):
+    torch, P = torch_mod(), lib()
+    from weight_only_quantization_w4a16_b200 import build
+    rel, dbg = P.load_library(), P.load_library(build.build(debug_bounds=True))
+    c = Layer(*shape)
+    y = c()
+    try:
+        P._lib = dbg
+        z = c()
+        status = P.awq_poll_device_status()
+    finally:
+        P._lib = rel
+    assert status == P.AWQ_OK and torch.equal(y, z)
