@@ -249,3 +249,24 @@ FORMS = [(1, 130, 528), (1, 25, 528), (19, 25, 16), (19, 130, 1040), (19, 38001,
 @pytest.mark.parametrize("M,N,K", FORMS)
 def test_product_forms(M, N, K):
     test_product(M, N, K)
+
+
+def test_two_streams_repeat_every_result():
+    """One token and a prompt, queued on two streams: each result equals the one before it of the same layer."""
+    torch, P = torch_mod(), lib()
+    rng = np.random.default_rng(22)
+    work = []
+    for M, N, K in ((1, 4096, 2048), (300, 1000, 528)):
+        W, x = (rng.standard_normal((n, K)).astype(np.float16) for n in (N, M))
+        work.append((P.AWQInt8Linear.from_float(dev(W)), dev(x), torch.cuda.Stream(), B.w8a8(*B.quantize_rows(x), *B.quantize_rows(W))))
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(20):
+        for layer, x, s, _ in work:
+            with torch.cuda.stream(s):
+                out.append(layer(x))
+    torch.cuda.synchronize()
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    for y, (_, _, _, ref) in zip(out[-2:], work):
+        check_y(y, ref)
+    assert all(torch.equal(a, b) for a, b in zip(out, out[2:]))

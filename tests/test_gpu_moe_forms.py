@@ -231,3 +231,21 @@ def test_forms_in_the_bounds_checked_build(shape):
     finally:
         P._lib = rel
     assert status == P.AWQ_OK and torch.equal(y, z)
+
+
+def test_two_streams_repeat_every_result():
+    """A few tokens and many, queued on two streams: each result equals the one before it of the same layer."""
+    torch, P = torch_mod(), lib()
+    c, d = Layer(4, 16, 4, 512, 384), Layer(32, 8, 2, 512, 640)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(20):
+        for layer, s in zip((c, d), streams):
+            with torch.cuda.stream(s):
+                out.append(layer())
+    torch.cuda.synchronize()
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    c.check(out[-2])
+    d.check(out[-1])
+    assert all(torch.equal(a, b) for a, b in zip(out, out[2:]))
