@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(1024) awq_quantize_rows_kernel(const __half* _
   const size_t row = blockIdx.x;
   const __half* xr = x + row * K;
   const int chunks = K / 8, tid = threadIdx.x, nthr = blockDim.x;
+  auto inside = [&](int c) { return AWQ_CHECK(c >= 0 && 8 * c + 8 <= K && row < gridDim.x); };
   constexpr int V = VPT > 0 ? VPT : 1;
   uint4 v[V];
   uint32_t m = 0;
@@ -110,16 +111,16 @@ __global__ void __launch_bounds__(1024) awq_quantize_rows_kernel(const __half* _
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * nthr;
-      v[i] = c < chunks ? ldg_stream_v4(xr + c * 8) : make_uint4(0, 0, 0, 0);
+      v[i] = c < chunks && inside(c) ? ldg_stream_v4(xr + c * 8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * nthr;
-      if (MODE != kRowPlain && c < chunks) v[i] = row_scaled<MODE>(v[i], s, c * 8);
+      if (MODE != kRowPlain && c < chunks && inside(c)) v[i] = row_scaled<MODE>(v[i], s, c * 8);
       m = max_abs_bits(m, v[i]);
     }
   } else {
-    for (int c = tid; c < chunks; c += nthr)
+    for (int c = tid; c < chunks && inside(c); c += nthr)
       m = max_abs_bits(m, row_scaled<MODE>(__ldg(reinterpret_cast<const uint4*>(xr + c * 8)), s, c * 8));
   }
   m = __vmaxu2(m, (m >> 16) | (m << 16)) & 0xFFFFu;
@@ -142,10 +143,10 @@ __global__ void __launch_bounds__(1024) awq_quantize_rows_kernel(const __half* _
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = tid + i * nthr;
-      if (c < chunks) store(c, v[i]);
+      if (c < chunks && inside(c)) store(c, v[i]);
     }
   } else {
-    for (int c = tid; c < chunks; c += nthr)
+    for (int c = tid; c < chunks && inside(c); c += nthr)
       store(c, row_scaled<MODE>(__ldg(reinterpret_cast<const uint4*>(xr + c * 8)), s, c * 8));
   }
   if (kWeights) __threadfence();
@@ -333,11 +334,13 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     auto issue_w = [&](int slot, int row, int kb, int n) {
+      if (!AWQ_CHECK(slot >= 0 && slot < S && n >= 1 && n <= kpb && row >= 0 && row < a.N && kb >= kb0 && kb + n <= kb1)) return;
       const uint32_t dst = base + slot * stage_bytes, bar = full0 + 8 * slot;
       mbar_expect_tx_at(bar, static_cast<uint32_t>(n * (a_bytes + b_bytes)));
       for (int j = 0; j < n; ++j) tma_load_2d_at(dst + j * a_bytes, &tmap_w, (kb + j) * 128, row, bar);
     };
     auto issue_x = [&](int slot, int row, int kb, int n) {
+      if (!AWQ_CHECK(slot >= 0 && slot < S && n >= 1 && n <= kpb && row >= 0 && row < a.M && kb >= kb0 && kb + n <= kb1)) return;
       const uint32_t dst = base + slot * stage_bytes + kpb * a_bytes, bar = full0 + 8 * slot;
       for (int j = 0; j < n; ++j) tma_load_2d_at(dst + j * b_bytes, &tmap_x, (kb + j) * 128, row, bar);
     };
@@ -429,6 +432,8 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
     // channels in pairs: with an even N, the lanes of a pair trade values of two tokens, so that each
     // stores both channels of one token in four bytes
     const bool paired = (a.N & 1) == 0;
+    // whether an output lies inside y (bounds-checked builds)
+    auto inside = [&](long long n, int tok) { return AWQ_CHECK(n >= 0 && n < a.N && tok >= 0 && tok < a.M); };
     bool ok = true;
     int it = 0;
     for (int t = tile0; ok && t < ntiles; t += step, ++it) {
@@ -459,8 +464,10 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
           tc_wait_ld();
           if (ks > 1) {                                      // the ring is idle: partial sums take its place
             int* part = reinterpret_cast<int*>(smem) + (m * BT + cw * C::kCols + c0) * 128 + 32 * e + lane;
+            if (AWQ_CHECK(static_cast<int>(reinterpret_cast<uint8_t*>(part + (CH - 1) * 128 + 1) - smem) <= ring_bytes)) {
 #pragma unroll
-            for (int j = 0; j < CH; ++j) part[j * 128] = static_cast<int>(v[j]);
+              for (int j = 0; j < CH; ++j) part[j * 128] = static_cast<int>(v[j]);
+            }
             continue;
           }
           __half o[CH];
@@ -482,13 +489,13 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
               const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
               // even lanes: token j of both channels; odd lanes: token j + 1
               const uint32_t w = odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-              if (n_ok && j < left) *reinterpret_cast<uint32_t*>(p) = w;
+              if (n_ok && j < left && inside(n + 1 - odd, tok0 + c0 + j + odd)) *reinterpret_cast<uint32_t*>(p) = w;
               p += 2 * static_cast<size_t>(a.N);
             }
           } else if (n_ok) {
 #pragma unroll
             for (int j = 0; j < CH; ++j)
-              if (tok0 + c0 + j < a.M) a.y[static_cast<size_t>(tok0 + c0 + j) * a.N + n] = o[j];
+              if (tok0 + c0 + j < a.M && inside(n, tok0 + c0 + j)) a.y[static_cast<size_t>(tok0 + c0 + j) * a.N + n] = o[j];
           }
         }
       }
@@ -517,6 +524,7 @@ __global__ void __launch_bounds__(Int8Cfg<BT, MT>::kThreads, 1)
         const int c = c_lo + i / quads, lr = i % quads * 4;   // four rows of one column
         const long long n = static_cast<long long>(rb) * kRows + lr;
         const uint32_t off = base + (((lr >> 7) * BT + c) * 128 + (lr & 127)) * 4;
+        if (!AWQ_CHECK(c >= 0 && tt * BT + c < a.M && off - base + 16 <= static_cast<uint32_t>(ring_bytes))) continue;
         int4 v[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {

@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         const int p0 = what.w * k.len, n = what.z * min(k.len, k.Q - p0);      // items of a half
         stage_of[slot] = what;
         mbar_arrive_expect_tx(&full[slot], 2 * n * kItem);
-        if (n > 0) {
+        if (n > 0 && AWQ_CHECK(what.x >= 0 && what.x < V && slot < S)) {
           size_t tp = static_cast<size_t>(l_expert[what.x]) * pairs + static_cast<size_t>(what.y) * k.Q + p0;
           for (int h = 0; h < 2; ++h) {
             if (AWQ_CHECK(n <= kMoeTile && tp + n <= a.E * pairs)) {
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
             for (int q = lane0; q < (16 * cnt) << k1.shift; q += 32 * kMoeEpi) {
               const int row = q & 15, i = (q >> 4) & (k1.strips - 1), col = q >> (4 + k1.shift);
               const int i_row = 16 * (what.y + i) + row;
-              if (i >= nu || !AWQ_CHECK(first + col < n_assign && i_row < a.I)) continue;
+              if (i >= nu || !AWQ_CHECK(first + col < n_assign && i_row < a.I && i * k1.wide + k1.len <= kMoeCW)) continue;
               const float code = row < 8 ? 16777216.0f : 1048576.0f;           // the factors that the codes carry
               const float g = code * sum(0, i * k1.wide, k1.len, col, row), v = code * sum(1, i * k1.wide, k1.len, col, row);
               float hv = silu_mul(g, v);
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
             for (int q = lane0; q < (32 * cnt) << k2.shift; q += 32 * kMoeEpi) {
               const int row = q & 15, i = (q >> 4) & (k2.strips - 1), half = (q >> (4 + k2.shift)) & 1, col = q >> (5 + k2.shift);
               const int k = 16 * (half * (a.K / 32) + what.y + i) + row;
-              if (i >= nu || !AWQ_CHECK(first + col < n_assign && k < a.K)) continue;
+              if (i >= nu || !AWQ_CHECK(first + col < n_assign && k < a.K && i * k2.wide + nw <= kMoeCW && what.w < k2.chunks)) continue;
               a.part[(static_cast<size_t>(first + col) * k2.chunks + what.w) * a.K + k] =
                   l_p[first + col] * sum(half, i * k2.wide, nw, col, row);
             }
@@ -708,6 +708,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   };
   // columns past a block's last token repeat it; they are never used
   auto slot_of = [&](int x) { return l_first[x] + min(r, l_first[x + 1] - l_first[x] - 1); };
+  // whether a slot and a pair of groups lie inside the lists and the rows
+  auto inside = [&](int s, int pr, const MoeCut& k) {
+    return s >= 0 && s < n_assign && l_token[s] >= 0 && l_token[s] < a.T && pr >= 0 && pr < k.Q;
+  };
   const uint8_t* const item0 = smem + lane * 16;
   auto load_item = [&](uint4 (&w)[2], uint32_t& sv, uint32_t& zz, const uint8_t* sb, int item, int h, int g) {
     const uint8_t* c = sb + (item + h * kMoeTile) * kPairCodeBytes + g * 1024;
@@ -731,9 +735,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
           fx = what.x;
           fc = what.w;
           mine = pl < k1.len && fc * k1.len + pl < k1.Q;
-          if (mine) load_frag(f, a.x + static_cast<size_t>(l_token[slot_of(fx)]) * a.K, fc * k1.len + pl, a.K / kGroup);
+          if (mine && AWQ_CHECK(inside(slot_of(fx), fc * k1.len + pl, k1)))
+            load_frag(f, a.x + static_cast<size_t>(l_token[slot_of(fx)]) * a.K, fc * k1.len + pl, a.K / kGroup);
         }
-        if (mine && sub < what.z) {
+        if (mine && sub < what.z && AWQ_CHECK(item < kMoeTile)) {
           const uint8_t* sb = item0 + slot * kMoeStage;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -769,10 +774,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
         fx = what.x;
         fc = what.w;
         mine = pl < k2.len && fc * k2.len + pl < k2.Q;
-        if (mine) load_ints(f, a.h + static_cast<size_t>(slot_of(fx)) * a.I, fc * k2.len + pl, a.I / kGroup);
+        if (mine && AWQ_CHECK(inside(slot_of(fx), fc * k2.len + pl, k2)))
+          load_ints(f, a.h + static_cast<size_t>(slot_of(fx)) * a.I, fc * k2.len + pl, a.I / kGroup);
       }
       if (!warp_wait(&rempty[rbuf], rphase ^ 1)) return false;
-      const bool has = mine && sub < what.z;
+      const bool has = mine && sub < what.z && AWQ_CHECK(item < kMoeTile);
       const uint8_t* sb = item0 + slot * kMoeStage;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -811,7 +817,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = min(n + j, terms - 1) / k2.chunks, c = min(n + j, terms - 1) - i * k2.chunks;
-        w[j] = ld_coherent_v4(a.part + (static_cast<size_t>(of[i]) * k2.chunks + c) * a.K + k4);
+        w[j] = AWQ_CHECK(of[i] >= 0 && of[i] < n_assign && c < k2.chunks && k4 + 4 <= a.K && tok < a.T)
+                   ? ld_coherent_v4(a.part + (static_cast<size_t>(of[i]) * k2.chunks + c) * a.K + k4)
+                   : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

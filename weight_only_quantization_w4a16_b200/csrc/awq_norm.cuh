@@ -80,12 +80,13 @@ __global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kerne
   const float inv_k = 1.0f / static_cast<float>(a.K);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const size_t base = row * a.K;
+  auto inside = [&](int c) { return AWQ_CHECK(c >= 0 && 8 * c + 8 <= a.K && row < gridDim.x); };
   uint4 yv[VPT], rv[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * nthr;
-    yv[i] = c < chunks ? ldg_stream_v4(a.y + base + c * 8) : zero;
-    rv[i] = c < chunks && a.residual != nullptr ? ldg_stream_v4(a.residual + base + c * 8) : zero;
+    yv[i] = c < chunks && inside(c) ? ldg_stream_v4(a.y + base + c * 8) : zero;
+    rv[i] = c < chunks && a.residual != nullptr && inside(c) ? ldg_stream_v4(a.residual + base + c * 8) : zero;
   }
   float rstd = 1.0f;
   if (a.post_w != nullptr) {
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kerne
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = tid + i * nthr;
-        if (c < chunks && (c & 7) == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(g + c * 8));
+        if (c < chunks && (c & 7) == 0 && inside(c)) asm volatile("prefetch.global.L2 [%0];" ::"l"(g + c * 8));
       }
     }
     float sum = 0.0f;
@@ -116,13 +117,13 @@ __global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kerne
     float r[8];
     unpack8(yv[i], h[i]);
     unpack8(rv[i], r);
-    if (a.post_w != nullptr && c < chunks) {
+    if (a.post_w != nullptr && c < chunks && inside(c)) {
       float w[8];
       unpack8(__ldg(reinterpret_cast<const uint4*>(a.post_w + c * 8)), w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = h[i][j] * rstd * w[j];
     }
-    if (gate != nullptr && c < chunks) {
+    if (gate != nullptr && c < chunks && inside(c)) {
       float g[8];
       unpack8(__ldg(reinterpret_cast<const uint4*>(gate + c * 8)), g);
 #pragma unroll
@@ -133,13 +134,13 @@ __global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kerne
       h[i][j] = fmaf(a.alpha, h[i][j], r[j]);
       sum = fmaf(h[i][j], h[i][j], sum);
     }
-    if (a.h != nullptr && c < chunks) *reinterpret_cast<uint4*>(a.h + base + c * 8) = pack8(h[i]);
+    if (a.h != nullptr && c < chunks && inside(c)) *reinterpret_cast<uint4*>(a.h + base + c * 8) = pack8(h[i]);
   }
   rstd = __frsqrt_rn(fmaf(block_sum(sum, s_part[1]), inv_k, a.eps));
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * nthr;
-    if (c >= chunks) continue;
+    if (c >= chunks || !inside(c)) continue;
     float w[8];
     unpack8(__ldg(reinterpret_cast<const uint4*>(a.w + c * 8)), w);
 #pragma unroll
