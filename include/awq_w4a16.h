@@ -310,8 +310,8 @@ AWQ_API awq_status_t awq_search_alpha_noalloc(const uint16_t* x, const uint16_t*
  * awq_w8a8_forward: awq_quantize_tokens, then awq_w8a8_linear, for a whole layer in one call. Its
  *   workspace (device, 16-byte aligned, awq_w8a8_workspace_bytes: M*K rounded up to 256, + 4*M)
  *   receives xq, then sx.
- * Require M >= 1, N >= 1 (both at most 2^31 - 128), 16 <= K <= AWQ_INT8_MAX_K, K % 16 == 0; x, s, W,
- * xq, wq and y 16-byte aligned. */
+ * Require M >= 1, N >= 1 (both at most 2^31 - 128), M * N <= 2^40, 16 <= K <= AWQ_INT8_MAX_K, K % 16 == 0;
+ * x, s, W, xq, wq and y 16-byte aligned. */
 #define AWQ_INT8_MAX_K 131056   /* (-128)^2 K < 2^31 */
 AWQ_API awq_status_t awq_quantize_tokens(const uint16_t* x, const float* s, int M, int K, int8_t* xq, float* sx,
                                          awq_stream_t stream);

@@ -193,3 +193,15 @@ def test_expert_layer_on_another_device_is_refused():
     layer.router = half(8, 256)
     with pytest.raises((TypeError, ValueError, RuntimeError), match="router"):
         layer(half(3, 256))
+
+
+def test_w8a8_refuses_more_outputs_than_its_tiles_can_count(lib):
+    """M N is at most 2^40, and both sizes are taken up to 2^31 - 128."""
+    top = 2 ** 31 - 128
+    assert lib.awq_w8a8_linear(*[V(A)] * 5, top, top, 16, None) == 1
+    assert lib.awq_w8a8_linear(*[V(A)] * 5, 2 ** 20 + 1, 2 ** 20, 16, None) == 1
+    assert lib.awq_w8a8_linear(*[V(A)] * 5, top + 1, 1, 16, None) == 1
+    assert lib.awq_w8a8_linear(*[V(A)] * 5, 1, top + 1, 16, None) == 1
+    # with the sizes in range the next check answers
+    for M, N in ((top, 1), (1, top), (2 ** 20, 2 ** 20)):
+        assert lib.awq_w8a8_linear(V(MIS), *[V(A)] * 4, M, N, 16, None) == 3

@@ -270,3 +270,23 @@ def test_two_streams_repeat_every_result():
     for y, (_, _, _, ref) in zip(out[-2:], work):
         check_y(y, ref)
     assert all(torch.equal(a, b) for a, b in zip(out, out[2:]))
+
+
+@pytest.mark.parametrize("side", ["tokens", "channels"])
+def test_most_tokens_and_channels(side):
+    """2^31 - 128 rows of one operand: a tile of 256 rows ends just below 2^31."""
+    torch, P = torch_mod(), lib()
+    top, K, few = 2 ** 31 - 128, 16, 300
+    rng = np.random.default_rng(31)
+    tail, one = (rng.integers(-127, 128, (n, K)).astype(np.int8) for n in (few, 1))
+    step, unit = rng.uniform(0.5, 2, few).astype(np.float32) * 1e-3, np.full(1, 0.5, np.float32)
+    big = torch.zeros((top, K), dtype=torch.int8, device="cuda")
+    steps = torch.ones(top, device="cuda")
+    big[-few:], steps[-few:] = dev(tail), dev(step)
+    y = P.awq_w8a8_linear(*((big, steps, dev(one), dev(unit)) if side == "tokens" else (dev(one), dev(unit), big, steps)))
+    assert P.awq_poll_device_status() == P.AWQ_OK
+    y = y.view(-1)
+    check_y(y[-few:], B.w8a8(tail, step, one, unit).reshape(-1))
+    assert not y[:-few].any()
+    del big, steps, y
+    torch.cuda.empty_cache()

@@ -28,7 +28,8 @@ constexpr int kPairCodeBytes = 2048;   // codes of one (tile, group pair)
 constexpr int kPairScaleBytes = 64;    // scales of one (tile, group pair)
 constexpr int kPairZeroBytes = 16;     // zeros of one (tile, group pair)
 
-__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// for a >= 0 up to INT_MAX, as a + b - 1 may pass it
+__host__ __device__ inline int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 // Rows rounded up to whole 128-row super-tiles (the prefill kernel's and the quantizer's row blocks).
 __host__ __device__ inline int padded_rows(int N) { return ceil_div(N, kSuperRows) * kSuperRows; }
 

@@ -651,7 +651,6 @@ awq_status_t launch_w8a8_cfg(const int8_t* xq, const float* sx, const int8_t* wq
   const int cap = BT <= 64 ? kI8SmemMax / 2 : kI8SmemMax;
   a.stages = std::max(2, std::min(kI8MaxStages, (cap - kI8Fixed - pad) / (a.kpb * block)));
   const long long tiles = static_cast<long long>(a.row_blocks) * a.tok_tiles;
-  if (tiles * p.ks > (1ll << 30)) return AWQ_ERR_INVALID_ARG;
   const size_t smem = static_cast<size_t>(a.stages) * a.kpb * block + pad + kI8Fixed;
   CUtensorMap wmap, xmap;
   if ((st = make_i8_map(&wmap, wq, N, K, p.rows)) != AWQ_OK) return st;
@@ -709,7 +708,8 @@ awq_status_t check_w8a8_args(const void* xq, const void* sx, const void* wq, con
                              int K) {
   if (!xq || !sx || !wq || !sw || !y) return AWQ_ERR_INVALID_ARG;
   if (M < 1 || N < 1 || N > kMaxRows || K < 16 || K % 16 != 0 || K > AWQ_INT8_MAX_K) return AWQ_ERR_INVALID_ARG;
-  if (M > kMaxRows) return AWQ_ERR_INVALID_ARG;
+  // M N <= 2^40 keeps the tiles' count, at most M N / 2^13 + N / 2^7 + M / 2^6 + 1, below 2^28
+  if (M > kMaxRows || static_cast<long long>(M) * N > (1ll << 40)) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(xq) || !aligned16(wq) || !aligned16(y) || (reinterpret_cast<uintptr_t>(sx) & 3u) ||
       (reinterpret_cast<uintptr_t>(sw) & 3u))
     return AWQ_ERR_MISALIGNED;
