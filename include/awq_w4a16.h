@@ -42,7 +42,7 @@
  *     argument returns an error code and launches nothing. No call aborts the
  *     process or throws.
  *   - fp16 buffers hold IEEE binary16 bit patterns (uint16_t here).
- *   - Outputs must not alias inputs.
+ *   - Outputs must not alias inputs (awq_residual_norm allows it, see there).
  *   - Only device ordinals with compute capability 10.0 are supported
  *     (AWQ_ERR_UNSUPPORTED otherwise).
  *
@@ -330,7 +330,8 @@ AWQ_API awq_status_t awq_w8a8_forward(const uint16_t* x, const float* s, const i
  *   h  = residual + alpha * gate * t
  *   x  = h / sqrt(mean_k(h^2) + eps) * weight / s
  * in fp32, each of h and x rounded once to fp16 (x is computed from the unrounded h).
- *   y, residual, h, x  fp16 [M, K] row-major; residual NULL: 0; h NULL: not stored.
+ *   y, residual, h, x  fp16 [M, K] row-major; residual NULL: 0; h NULL: not stored. In place: h may be
+ *         the residual's buffer or y's, and x the other one; any other overlap of an output is not allowed.
  *   gate  fp16 [ceil(M / rows_per_gate), K] or NULL (1): row m uses gate row m / rows_per_gate
  *         (rows_per_gate = 1: a gate per token; >= M: one row for all; in between: one per sequence).
  *   post_weight, weight  fp16 [K] (post_weight may be NULL);  s fp32 [K] or NULL (1).

@@ -205,3 +205,21 @@ def test_w8a8_refuses_more_outputs_than_its_tiles_can_count(lib):
     # with the sizes in range the next check answers
     for M, N in ((top, 1), (1, top), (2 ** 20, 2 ** 20)):
         assert lib.awq_w8a8_linear(V(MIS), *[V(A)] * 4, M, N, 16, None) == 3
+
+
+def test_norm_outputs_in_place_and_other_overlaps():
+    """An output may be y or the residual themselves; any other overlap is refused."""
+    flat = half(200)
+    y, r, w, g = half(6, 16), half(6, 16), half(16), half(6, 16)
+
+    def check(h, x, y=y, residual=r, gate=None, s=None, post=None):
+        P.validate_residual_norm(y, residual, w, post, gate, 1.0, 1e-6, s, h, x, require_cuda=False)
+
+    for h, x in ((r, y), (y, r), (r, half(6, 16)), (half(6, 16), y), (None, r), (None, y)):
+        check(h, x)
+    a, b = flat[:96].view(6, 16), flat[16:112].view(6, 16)
+    for h, x, kw in ((b, half(6, 16), dict(residual=a)), (half(6, 16), b, dict(y=a)), (y, y, {}), (a, b, {}), (g, y, dict(gate=g)),
+                     (r, g, dict(gate=g)), (r, half(6, 16), dict(residual=None, gate=r)), (a, y, dict(post=a[0])),
+                     (a, y, dict(s=a[:2].reshape(-1).view(torch.float32)))):
+        with pytest.raises(ValueError, match="overlap"):
+            check(h, x, **kw)

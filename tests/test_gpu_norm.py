@@ -173,3 +173,23 @@ def test_gate_and_post_weight_refusals_on_the_device():
                 dict(post_weight=half(63)), dict(post_weight=half(1, 64)), dict(post_weight=half(64).float())):
         with pytest.raises((ValueError, TypeError)):
             P.awq_residual_norm(y, y, half(64), **bad)
+
+
+@pytest.mark.parametrize("M,K", [(1, 4096), (3, 12296), (600, 4104), (2400, 4104), (2, 32768)])
+@pytest.mark.parametrize("post,gates", [(False, 0), (True, -1)])
+def test_in_place(M, K, post, gates):
+    """h in the residual's buffer and x in y's, or the other way round: the bits of the call with buffers of its own."""
+    torch, P = torch_mod(), lib()
+    gen = torch.Generator("cuda").manual_seed(M + K)
+    rand = lambda *shape: torch.randn(shape, device="cuda", generator=gen).half()  # noqa: E731
+    y, r, w = rand(M, K), rand(M, K), rand(K)
+    kw = dict(post_weight=w if post else None, gate=rand(M, K) if gates else None, alpha=0.7, s=rand(K).float().abs() + 0.1)
+    h, x = P.awq_residual_norm(y, r, w, **kw)
+    for swap in (False, True):
+        a, b = y.clone(), r.clone()
+        out = (a, b) if swap else (b, a)
+        got = P.awq_residual_norm(a, b, w, out=out, **kw)
+        assert got[0] is out[0] and torch.equal(out[0], h) and torch.equal(out[1], x)
+    b = r.clone()
+    _, x2 = P.awq_residual_norm(y, b, w, out=(b, torch.empty_like(y)), **kw)
+    assert torch.equal(b, h) and torch.equal(x2, x)

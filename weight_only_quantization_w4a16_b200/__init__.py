@@ -690,6 +690,14 @@ def _w8a8_forward(x, wq, sw, s, y, workspace):
 NORM_MAX_K = 32768
 
 
+def _overlap(a, b) -> bool:
+    """Whether two contiguous tensors share memory (False if one is None)."""
+    if a is None or b is None:
+        return False
+    pa, pb = a.data_ptr(), b.data_ptr()
+    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
 def validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x, require_cuda=True):
     torch = _torch()
     f16 = torch.float16
@@ -718,6 +726,13 @@ def validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s
                              f"got {tuple(gate.shape)}")
     if s is not None:
         _check_vec(s, K, "s", require_cuda)
+    for t, name, others in ((h, "h", (x,)), (x, "x", (h,))):
+        if t is None:
+            continue
+        if any(_overlap(t, v) and t.data_ptr() != v.data_ptr() for v in (y, residual)):
+            raise ValueError(f"{name} may be y or residual themselves, but not overlap a part of them")
+        if any(_overlap(t, v) for v in (*others, gate, post_weight, weight, s)):
+            raise ValueError(f"{name} must not overlap the other output, the gate or the weights")
     if not (-3.0e38 <= alpha <= 3.0e38) or not (0.0 <= eps <= 3.0e38):
         raise ValueError("alpha must be finite, and eps finite and not negative")
 
@@ -729,7 +744,8 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
     h = residual + alpha * gate * t with t = y, or y normalised and times ``post_weight`` if given;
     x' = rmsnorm(h) * weight / s. ``residual`` may be None (0); ``gate`` is None (1) or [G, K] with G a
     divisor of M: row m uses gate row m // (M // G). ``s`` is the next layer's stored scale.
-    ``want_h=False`` leaves h unstored (the first result is None)."""
+    ``want_h=False`` leaves h unstored (the first result is None). ``out=(h, x')``: in place with
+    ``out=(residual, y)`` (or either of them)."""
     torch = _torch()
     h = x = None
     if out is not None:

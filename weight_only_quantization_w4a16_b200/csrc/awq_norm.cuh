@@ -9,7 +9,8 @@
 // scaled down by s), so x' goes straight into a quantized linear call.
 //
 // Bound by HBM: 8 bytes per value (10 with a gate per token). One CTA per row; the row stays in
-// registers between the two means, so every input is read once. Few rows (a decoding batch) are bound
+// registers between the two means, so every input is read once, and a thread has read its values of y and
+// the residual before it writes h and x there: both may be updated in place. Few rows (a decoding batch) are bound
 // by latency and take as many threads as they have 8-value chunks; many rows two chunks per thread,
 // four where the norm after the block adds a second reduction and many rows hide it.
 // Measured: 8192 x 8192 83 us (0.98 of the copy rate; 95 with the IEEE division by s), 90 us with the
@@ -85,8 +86,8 @@ __global__ void __launch_bounds__(norm_max_threads(VPT)) awq_residual_norm_kerne
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = tid + i * nthr;
-    yv[i] = c < chunks && inside(c) ? ldg_stream_v4(a.y + base + c * 8) : zero;
-    rv[i] = c < chunks && a.residual != nullptr && inside(c) ? ldg_stream_v4(a.residual + base + c * 8) : zero;
+    yv[i] = c < chunks && inside(c) ? ld_stream_v4(a.y + base + c * 8) : zero;
+    rv[i] = c < chunks && a.residual != nullptr && inside(c) ? ld_stream_v4(a.residual + base + c * 8) : zero;
   }
   float rstd = 1.0f;
   if (a.post_w != nullptr) {
