@@ -335,9 +335,11 @@ AWQ_API awq_status_t awq_w8a8_forward(const uint16_t* x, const float* s, const i
  *   gate  fp16 [ceil(M / rows_per_gate), K] or NULL (1): row m uses gate row m / rows_per_gate
  *         (rows_per_gate = 1: a gate per token; >= M: one row for all; in between: one per sequence).
  *   post_weight, weight  fp16 [K] (post_weight may be NULL);  s fp32 [K] or NULL (1).
- * Requires M >= 1, 8 <= K <= AWQ_NORM_MAX_K, K % 8 == 0, alpha finite, eps finite and >= 0, and
+ * Requires M >= 1, 8 <= K <= AWQ_NORM_MAX_K, K % 8 == 0, |alpha| <= AWQ_NORM_MAX_ALPHA (the
+ * sums of squares then stay in fp32's range whatever the finite inputs are), eps finite and >= 0, and
  * rows_per_gate >= 1 where there is a gate; every pointer 16-byte aligned. */
 #define AWQ_NORM_MAX_K 32768
+#define AWQ_NORM_MAX_ALPHA 16777216.0f
 AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, const uint16_t* gate,
                                        int rows_per_gate, const uint16_t* post_weight, const uint16_t* weight,
                                        const float* s, float alpha, float eps, int M, int K, uint16_t* h, uint16_t* x,

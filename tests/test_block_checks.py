@@ -223,3 +223,11 @@ def test_norm_outputs_in_place_and_other_overlaps():
                      (a, y, dict(s=a[:2].reshape(-1).view(torch.float32)))):
         with pytest.raises(ValueError, match="overlap"):
             check(h, x, **kw)
+
+
+def test_norm_refuses_an_alpha_that_overflows_the_sum_of_squares(lib):
+    assert _norm(lib, alpha=1.0e15) == 1 and _norm(lib, alpha=-16777218.0) == 1
+    assert _norm(lib, alpha=-16777216.0, y=MIS) == 3           # in range: the next check answers
+    for alpha in (1.0e15, -16777218.0):
+        with pytest.raises(ValueError, match="alpha"):
+            P.validate_residual_norm(half(6, 16), None, half(16), None, None, alpha, 1e-6, None, None, None, require_cuda=False)

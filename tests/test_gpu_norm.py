@@ -193,3 +193,16 @@ def test_in_place(M, K, post, gates):
     b = r.clone()
     _, x2 = P.awq_residual_norm(y, b, w, out=(b, torch.empty_like(y)), **kw)
     assert torch.equal(b, h) and torch.equal(x2, x)
+
+
+def test_largest_inputs_and_alpha():
+    """The largest alpha, gate, y and K: h is past fp16, and x is still the normalised row."""
+    P = lib()
+    K = P.NORM_MAX_K
+    a = inputs(2, K, False, 1, False)
+    sign = np.sign(a["y"].astype(np.float32))
+    sign[sign == 0] = 1
+    a["y"], a["gate"] = (65504 * sign).astype(np.float16), np.full((1, K), 65504, np.float16)
+    h, x = P.awq_residual_norm(**to_dev(a), alpha=P.NORM_MAX_ALPHA)
+    assert np.isinf(host(h)).all()
+    check((None, x), a, "largest alpha", alpha=P.NORM_MAX_ALPHA)

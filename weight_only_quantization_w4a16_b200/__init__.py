@@ -688,6 +688,7 @@ def _w8a8_forward(x, wq, sw, s, y, workspace):
 
 # ---------------------------------------------------------------------------- residual update and norms
 NORM_MAX_K = 32768
+NORM_MAX_ALPHA = 16777216.0
 
 
 def _overlap(a, b) -> bool:
@@ -733,8 +734,8 @@ def validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s
             raise ValueError(f"{name} may be y or residual themselves, but not overlap a part of them")
         if any(_overlap(t, v) for v in (*others, gate, post_weight, weight, s)):
             raise ValueError(f"{name} must not overlap the other output, the gate or the weights")
-    if not (-3.0e38 <= alpha <= 3.0e38) or not (0.0 <= eps <= 3.0e38):
-        raise ValueError("alpha must be finite, and eps finite and not negative")
+    if not abs(alpha) <= NORM_MAX_ALPHA or not (0.0 <= eps <= 3.0e38):
+        raise ValueError(f"alpha must be finite and at most {NORM_MAX_ALPHA:.0f} in magnitude, and eps finite and not negative")
 
 
 def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: float = 1.0, eps: float = 1e-6, s=None,
@@ -763,7 +764,8 @@ def awq_residual_norm(y, residual, weight, post_weight=None, gate=None, alpha: f
                 (s is None or _fits(s, torch.float32, 1, K, dev)) and
                 (post_weight is None or _fits(post_weight, f16, 1, K, dev)) and
                 (gate is None or (type(gate) is torch.Tensor and _fits(gate, f16, 2, gate.numel(), dev) and
-                                  gate.shape[1] == K and gate.shape[0] > 0 and M % gate.shape[0] == 0)) and -3.0e38 <= alpha <= 3.0e38 and 0.0 <= eps <= 3.0e38)
+                                  gate.shape[1] == K and gate.shape[0] > 0 and M % gate.shape[0] == 0)) and abs(alpha) <= NORM_MAX_ALPHA and
+                0.0 <= eps <= 3.0e38)
     if not fits:
         validate_residual_norm(y, residual, weight, post_weight, gate, alpha, eps, s, h, x)
         M, K = y.shape

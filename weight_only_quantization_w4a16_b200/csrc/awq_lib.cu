@@ -1121,7 +1121,8 @@ awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residual, cons
                                float eps, int M, int K, uint16_t* h, uint16_t* x, awq_stream_t stream) {
   if (!y || !weight || !x || M < 1 || K < 8 || K % 8 != 0 || K > AWQ_NORM_MAX_K) return AWQ_ERR_INVALID_ARG;
   if (gate != nullptr && rows_per_gate < 1) return AWQ_ERR_INVALID_ARG;
-  if (!(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f || !(eps >= 0.0f) || eps > 3.0e38f) return AWQ_ERR_INVALID_ARG;
+  // up to 2^24 the sum of h^2 stays finite for all finite inputs: K (2^24 65504^2 + 65504)^2 < 2^127.1
+  if (!(fabsf(alpha) <= AWQ_NORM_MAX_ALPHA) || !(eps >= 0.0f) || eps > 3.0e38f) return AWQ_ERR_INVALID_ARG;
   if (!aligned16(y) || !aligned16(residual) || !aligned16(gate) || !aligned16(post_weight) || !aligned16(weight) ||
       !aligned16(s) || !aligned16(h) || !aligned16(x))
     return AWQ_ERR_MISALIGNED;
