@@ -362,7 +362,8 @@ AWQ_API awq_status_t awq_residual_norm(const uint16_t* y, const uint16_t* residu
  * output is NaN if it has an infinite largest logit, a NaN one among the chosen, or, without renormalize,
  * a NaN one at all, or if one of its h is NaN or past fp32's range. Other tokens of the call are not affected.
  * One kernel, a cooperative launch with one CTA on every SM that waits (bounded, AWQ_ERR_TIMEOUT) for
- * all others after the router and after each of the two layers. Bitwise reproducible.
+ * all others after the router and after each of the two layers. Bitwise reproducible. After a wait that
+ * ran out, the results of calls that ran on the device's other streams at that time are undefined too.
  * Requires 1 <= T <= 32, 1 <= E <= 512, 1 <= top_k <= min(E, 16), K and I multiples of 128, each
  * expert's layers within awq_*_bytes' limits; every pointer 16-byte aligned. */
 AWQ_API size_t awq_moe_workspace_bytes(int T, int E, int K, int I, int top_k);

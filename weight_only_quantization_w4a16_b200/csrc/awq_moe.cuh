@@ -104,8 +104,11 @@ struct MoeCut {
 // Arrivals at the grid-wide barriers since the library was loaded. Every CTA of a launch arrives at
 // each barrier exactly once, also when it has given up a wait, so the count is a multiple of the grid
 // size between barriers. One counter is enough: a CTA takes more than half of an SM's shared memory
-// and the grid all SMs, so two launches never run at once, and none of a launch's CTAs ends before
-// all have arrived at its last barrier.
+// and the grid all SMs, so two launches never run at once as long as none of a launch's CTAs ends before
+// all have arrived at its last barrier. Only a CTA that has given up a wait does: a launch on another
+// stream may then start beside the ones that are late, count their arrivals as its own and pass a barrier
+// early. Its results are undefined like the first one's (the header says so); its accesses stay in bounds,
+// as the lists that it reads are its own CTA's, and later launches find a multiple of the grid size again.
 __device__ unsigned long long g_moe_arrivals = 0;
 static_assert(kMoeStages * kMoeStage > 114 * 1024, "two of these CTAs must not fit one SM");
 
