@@ -664,7 +664,10 @@ def validate_w8a8_forward(x, wq, sw, s, y, require_cuda=True):
 
 
 def awq_w8a8_forward(x, wq, sw, s=None, y=None, workspace=None):
-    """A whole 8-bit linear layer: awq_quantize_tokens(x, s), then awq_w8a8_linear, in one call."""
+    """A whole 8-bit linear layer: awq_quantize_tokens(x, s), then awq_w8a8_linear, in one call.
+
+    ``workspace``: int8, at least awq_w8a8_workspace_bytes(M, K) long, for the tokens' codes and steps;
+    allocated here if None. Calls that may overlap on the GPU need workspaces of their own."""
     validate_w8a8_forward(x, wq, sw, s, y)
     return _w8a8_forward(x, wq, sw, s, y, workspace)
 
@@ -858,7 +861,9 @@ def awq_moe_w4a16(x, router, gate_up, down, I: int, top_k: int, renormalize: boo
 
     x [T, K] fp16; router [E, K] fp16; gate_up and down: (qweight, scales, zeros) with the experts'
     packed arrays stacked along a first dimension (gate_up: 2 I x K layers, I gate rows then I up
-    rows; down: K x I); h_scale [E, I] fp32 divides the intermediate (the down layers' s)."""
+    rows; down: K x I); h_scale [E, I] fp32 divides the intermediate (the down layers' s).
+    ``workspace``: uint8, at least awq_moe_workspace_bytes(T, E, K, I, top_k) long; allocated here if
+    None. Calls that may overlap on the GPU need workspaces of their own."""
     I, top_k = int(I), int(top_k)
     E, K = _validate_moe_weights(router, gate_up, down, I, top_k, h_scale)
     _validate_moe_tokens(x, y, E, K)

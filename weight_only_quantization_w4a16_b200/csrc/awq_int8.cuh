@@ -164,11 +164,15 @@ __global__ void __launch_bounds__(1024) awq_quantize_rows_kernel(const __half* _
 // the int32 partial sums (exact in any order) of its share of the token columns from distributed
 // shared memory.
 //
-// Bound: up to 64 tokens by the weight bytes, long prompts by the tensor pipe (128 cycles per MMA at BT = 256) and, run without a pause, by the power
-// limit. In between the two issuing warps bound it: a wait, four MMAs and a commit took 728 cycles per k
-// block, whatever BT, while a single lane ran them; with a converged warp, elect.sync, a wait without the
-// deadline code inside and descriptors in 32 bits they take 530, and 390 per block when two blocks share a
-// stage. A second producer warp for the tokens was slower: its barrier is one more wait for the MMA warp.
+// Bound: up to 64 tokens by the weight bytes. Above, a 128-byte k block takes 390 cycles at 128 columns (32 KB
+// of operands), 600 at 256 (48 KB, of which 512 cycles are the tensor pipe's) and 559 for two CTAs of 64
+// columns on an SM (48 KB): 82 to 88 bytes per cycle into an SM in every form, which is what bounds them as
+// far as these figures tell; the tensor pipe is 78% busy. Run without a pause, the power limit comes on top
+// (4096 x 28672 x 4096: 337 us at first, 385 to 395 at the 1.4 GHz that it leaves). The issuing warps were the
+// bound before: a wait, four MMAs and a commit took 728 cycles per k block, whatever BT, while a single lane
+// ran them; 530 with a converged warp, elect.sync, a wait without the deadline code inside and descriptors in
+// 32 bits; 390 when two blocks share a stage. A second producer warp for the tokens was slower: its barrier
+// is one more wait for the MMA warp.
 // Rows that do not start on 128-byte lines (K % 128 != 0) cost the copies two lines per row: 3 cycles
 // per row and k block, which bounds 333 x 5001 x 4112.
 struct Int8Args {

@@ -590,9 +590,8 @@ awq_status_t make_i8_map(CUtensorMap* map, const void* q, int rows, int K, int b
 // among equals one without a K split, or else the larger split with the taller tiles (measured at M = 1:
 // 4096 x 14336 12.5 us with 256 CTAs against 17.2 with 64; 28672 x 4096 20.3 unsplit against 21.5;
 // 12288 x 4096 11.3 split four ways against 12.1 two ways).
-// Above, a 128-byte k block takes about `step` cycles: 256 token columns are bound by the tensor pipe, 128
-// and 64 by what the issuing warps do per block (600 and 420 cycles measured; a third more where two CTAs
-// share an SM). A K split saves rounds of a small grid but pays for the exchange (1500 + 30 per column:
+// Above, a 128-byte k block takes about `step` cycles: 600 with 256 token columns, 420 with 128 or 64 (a third
+// more where two CTAs share an SM), as measured. A K split saves rounds of a small grid but pays for the exchange (1500 + 30 per column:
 // 512 x 4096 x 14336 30.5 us with it, 44.4 without, at 256 columns), and never pays beyond one round.
 struct Int8Plan {
   int bt, mt, rows, ks;

@@ -13,6 +13,8 @@
 // the residual before it writes h and x there: both may be updated in place. Few rows (a decoding batch) are bound
 // by latency and take as many threads as they have 8-value chunks; many rows two chunks per thread,
 // four where the norm after the block adds a second reduction and many rows hide it.
+// (The division by s is approximate, 2 units of 2^-24, and gives 0 from |s| = 2^126 on, where x' is 0 in fp16
+// anyway.)
 // Measured: 8192 x 8192 83 us (0.98 of the copy rate; 95 with the IEEE division by s), 90 us with the
 // norm after the block (98 with two chunks per thread); 4096 x 8192 with both norms and a gate per token
 // 63 us (0.81), 68 without the gate's prefetch, which a few rows of one chunk per thread do not repay
