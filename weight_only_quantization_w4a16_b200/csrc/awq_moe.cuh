@@ -33,8 +33,8 @@
 // integers of h; 8 tokens 144 (floor 96); 32 tokens 212 to 218 (floor 112), bound by the consumers'
 // instructions, of which every block of 8 tokens has its own. 64 experts of 2048 x 1408, six per token, 5
 // tokens: 46 (floor 17). A warp's integers of h take 1300 to 2000 cycles each time it comes to another block
-// or part of K, which h in fp16 did in half of that (51, 138, 205 and 42 us): its rounding doubled the
-// output's squared error, and what lies below 2^-14 lost more, down to all of it.
+// or part of K. (With h in fp16 the calls took 51, 138, 205 and 42 us, but its rounding doubled the output's
+// squared error, and what lies below 2^-14 lost more, down to all of it.)
 //
 // The kernel neither starts before its predecessor has ended nor lets its successor start early: CTAs
 // that wait for it could otherwise hold the registers that its own last CTAs need, and the barrier
