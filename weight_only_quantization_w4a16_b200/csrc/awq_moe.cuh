@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) awq_moe_kernel(const MoeArgs a
   };
   // columns past a block's last token repeat it; they are never used
   auto slot_of = [&](int x) { return l_first[x] + min(r, l_first[x + 1] - l_first[x] - 1); };
-  // whether a slot and a pair of groups lie inside the lists and the rows
-  auto inside = [&](int s, int pr, const MoeCut& k) {
+  // whether a slot and a pair of groups lie inside the lists and the rows (bounds-checked builds)
+  [[maybe_unused]] auto inside = [&](int s, int pr, const MoeCut& k) {
     return s >= 0 && s < n_assign && l_token[s] >= 0 && l_token[s] < a.T && pr >= 0 && pr < k.Q;
   };
   const uint8_t* const item0 = smem + lane * 16;
